@@ -335,6 +335,125 @@ int compress24_host(int dtype, int64_t M, int64_t K, const void* A, int64_t lda,
 int decompress24_host(int dtype, int64_t M, int64_t K, const void* A_compressed, int64_t lda_c,
                       const uint32_t* A_index, int64_t ld_idx, void* A, int64_t lda);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The 8-bit linear layer: activations and weights as int8 codes with binary32
+ * scales, the products that use them, and what a training step needs of them.
+ * A row q of codes with the scale s stands for the values s * q.  Rows are
+ * tokens, columns are channels; every matrix is row-major with a leading
+ * dimension in elements, at any alignment of its elements.  All calls are
+ * deterministic: nothing is added atomically.
+ * ---------------------------------------------------------------------------
+ *
+ * rmsnorm_quant -- the root-mean-square norm of a sum, in 8 bits:
+ *     h = x + r,  rstd = (mean(h^2) + eps)^(-1/2),  y = h * weight * rstd
+ *     scale = max|y| / 127,  q = rint(y / scale)      (ties to even)
+ * for each of M rows of N channels.
+ *
+ * dtype         : MCG_BF16, MCG_F16 or MCG_F32, of X, R, weight and H.
+ * R, ldr        : the residual, or NULL (h = x).
+ * weight        : N values, or NULL (ones).
+ * eps           : finite, >= 0 (used as binary32).
+ * H, ldh        : h rounded once to dtype, or NULL.  H may be X or R (same
+ *                 pointer and leading dimension); other overlaps are undefined.
+ * Q, ldq, scale : codes (-127..127) and M scales.
+ * rstd          : M values, or NULL (kept for rmsnorm_backward).
+ * Squares and sums are binary32, taken of the sum h before it is rounded.  A row
+ * whose y is all zero has scale 0; a row with a NaN or an infinity, or whose
+ * squares leave binary32, has scale NaN and codes 0.  N == 0 gives scale 0.
+ */
+int rmsnorm_quant(int dtype, int64_t M, int64_t N, const void* X, int64_t ldx, const void* R, int64_t ldr,
+                  const void* weight, double eps, void* H, int64_t ldh, int8_t* Q, int64_t ldq, float* scale,
+                  float* rstd, void* stream);
+
+/*
+ * rmsnorm_backward -- gradient of y = x * rstd * weight over rows of N channels:
+ *     g = dy * weight,  dx = rstd * (g - x * rstd^2 * mean(g x)) + dr
+ *     dw = sum over the rows of dy * x * rstd
+ *
+ * dtype         : MCG_BF16, MCG_F16 or MCG_F32, of dY, weight, dR and dX.
+ * dtypeX, scaleX: dtype (scaleX ignored), or MCG_I8: X holds codes, M scales
+ *                 in scaleX (the norm's input as an 8-bit checkpoint).
+ * X             : the norm's input (rmsnorm_quant's h), rstd as it left it.
+ * weight        : N values, or NULL (ones).
+ * dR, lddr      : gradient that reaches the input past the norm, or NULL.
+ * dX            : may be dY or dR (same pointer and leading dimension).
+ * dW            : N binary32 values, written; or NULL.  Needs a workspace of
+ *                 mcg_rmsnorm_backward_workspace_bytes(M, N) bytes (16-byte
+ *                 aligned; MCG_ERR_SCRATCH_LIMIT otherwise), whose contents on
+ *                 entry do not matter; calls that share it must not overlap.
+ *                 M == 0 writes zeros.
+ * Sums are binary32 in a fixed order.
+ */
+int rmsnorm_backward(int dtype, int dtypeX, int64_t M, int64_t N, const void* dY, int64_t lddy, const void* X,
+                     int64_t ldx, const float* scaleX, const void* weight, const float* rstd, const void* dR,
+                     int64_t lddr, void* dX, int64_t lddx, float* dW, void* workspace, int64_t workspace_bytes,
+                     void* stream);
+int64_t mcg_rmsnorm_backward_workspace_bytes(int64_t M, int64_t N);
+
+/*
+ * quantize_rows / dequantize_rows -- the 8-bit checkpoint of an activation:
+ * scale = max|x| / 127 and q = rint(x / scale) for each row, and the values
+ * scale * q rounded once to dtypeD (MCG_BF16, MCG_F16 or MCG_F32).  Rows of
+ * zeros, NaN and infinities as for rmsnorm_quant (the values of a row with
+ * scale NaN are NaN).
+ */
+int quantize_rows(int dtype, int64_t M, int64_t N, const void* X, int64_t ldx, int8_t* Q, int64_t ldq, float* scale,
+                  void* stream);
+int dequantize_rows(int dtypeD, int64_t M, int64_t N, const int8_t* Q, int64_t ldq, const float* scale, void* D,
+                    int64_t ldd, void* stream);
+
+/*
+ * gemm_i8_scaled -- int8 product with a scale per token and channel:
+ *     D[i][j] = scaleA[i] * scaleB[j] * sum_k A[i][k] B[k][j] + bias[j]
+ *
+ * A             : M x K int8, row-major (activations).
+ * B             : K x N int8; layoutB as for gemm_dense (MCG_K_CONTIG: weights
+ *                 stored N x K).
+ * scaleA, scaleB: M and N binary32 values.  bias: N binary32 values, or NULL.
+ * dtypeD        : MCG_F32, MCG_BF16 or MCG_F16.
+ * K             : 0 .. 131071 (the int32 sum is exact; beyond it could wrap, and
+ *                 the call returns MCG_ERR_INVALID_SIZE).
+ * workspace     : 16-byte aligned device memory, or NULL; a call uses at most
+ *                 mcg_i8_scaled_workspace_bytes(...) of it to cut K over more
+ *                 workgroups, and less when less is given (the result is the
+ *                 same).  Contents irrelevant on entry, unspecified after; calls
+ *                 that share it must not overlap.
+ * Accuracy      : the exact integer sum is rounded to binary32, multiplied by
+ *                 scaleA, then by scaleB with the bias added in one fused step,
+ *                 and rounded to D's type.
+ */
+int gemm_i8_scaled(int layoutB, int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const float* scaleA,
+                   const int8_t* B, int64_t ldb, const float* scaleB, const float* bias, void* D, int64_t ldd,
+                   int dtypeD, void* workspace, int64_t workspace_bytes, void* stream);
+int64_t mcg_i8_scaled_workspace_bytes(int layoutB, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
+                                      const void* B, int64_t ldb);
+
+/*
+ * gemm_grad_i8 -- product of a 16-bit matrix with 8-bit rows:
+ *     D[i][j] = sum_k A[i][k] * (scaleK[k] * Q[k][j]) + beta * C[i][j]
+ * A linear layer's weight gradient from the 8-bit checkpoint of its input
+ * (A = dY stored K x M, k the tokens) and its input gradient from its 8-bit
+ * weights (A = dY stored M x K, k the output channels).
+ *
+ * dtypeA        : MCG_BF16 or MCG_F16.  layoutA: as for gemm_dense.
+ * Q, ldq        : K x N int8, row-major; scaleK: K binary32 values.
+ * dtypeD        : dtypeA or MCG_F32, of C and D (leading dimension ldd of both).
+ * beta, C       : C is read only when beta != 0; D may be C.
+ * workspace     : as for gemm_i8_scaled, mcg_grad_i8_workspace_bytes(...).
+ * Accuracy      : scaleK * Q is formed in binary32 and multiplied on the matrix
+ *                 cores in dtypeA: rounded once to it for a D of that type; as
+ *                 the sum of two such values for a binary32 D (2^-17 of a bf16
+ *                 value left, 2^-22 of an f16 value, and never less than f16's
+ *                 own spacing near zero).  With f16 the values must lie in its
+ *                 range.  Sums are binary32.
+ */
+int gemm_grad_i8(int dtypeA, int layoutA, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
+                 const int8_t* Q, int64_t ldq, const float* scaleK, const void* C, void* D, int64_t ldd, int dtypeD,
+                 double beta, void* workspace, int64_t workspace_bytes, void* stream);
+int64_t mcg_grad_i8_workspace_bytes(int dtypeA, int layoutA, int64_t M, int64_t N, int64_t K, const void* A,
+                                    int64_t lda, const void* Q, int64_t ldq, int dtypeD);
+
 /* Host-only argument checks: the exact validation the entry points above run
  * before touching the device (same arguments, minus outputs' contents and the
  * stream).  They never call HIP and return an mcg_status. */
@@ -349,6 +468,23 @@ int mcg_validate_sparse24(int dtypeA, int dtypeB, int layoutB, int64_t M, int64_
 int mcg_validate_compress24(int dtype, int64_t M, int64_t K, const void* A, int64_t lda,
                             const void* A_compressed, int64_t lda_c, const uint32_t* A_index,
                             int64_t ld_idx);
+int mcg_validate_rmsnorm_quant(int dtype, int64_t M, int64_t N, const void* X, int64_t ldx, const void* R,
+                               int64_t ldr, const void* weight, double eps, const void* H, int64_t ldh,
+                               const void* Q, int64_t ldq, const void* scale, const void* rstd);
+int mcg_validate_rmsnorm_backward(int dtype, int dtypeX, int64_t M, int64_t N, const void* dY, int64_t lddy,
+                                  const void* X, int64_t ldx, const void* scaleX, const void* weight,
+                                  const void* rstd, const void* dR, int64_t lddr, const void* dX, int64_t lddx,
+                                  const void* dW, const void* workspace, int64_t workspace_bytes);
+int mcg_validate_quantize_rows(int dtype, int64_t M, int64_t N, const void* X, int64_t ldx, const void* Q,
+                               int64_t ldq, const void* scale);
+int mcg_validate_dequantize_rows(int dtypeD, int64_t M, int64_t N, const void* Q, int64_t ldq, const void* scale,
+                                 const void* D, int64_t ldd);
+int mcg_validate_i8_scaled(int layoutB, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
+                           const void* scaleA, const void* B, int64_t ldb, const void* scaleB, const void* bias,
+                           const void* D, int64_t ldd, int dtypeD, const void* workspace, int64_t workspace_bytes);
+int mcg_validate_grad_i8(int dtypeA, int layoutA, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
+                         const void* Q, int64_t ldq, const void* scaleK, const void* C, const void* D, int64_t ldd,
+                         int dtypeD, double beta, const void* workspace, int64_t workspace_bytes);
 
 /* Kernel selection, for callers that tune shapes and for tests.  Host-only,
    no validation, no device memory access; the cost model uses the current

@@ -34,7 +34,12 @@ EXPORTS = ("gemm_dense", "gemm_dense_ws", "gemm_dense_noalloc", "mcg_dense_noall
            "mcg_status_string",
            "mcg_version", "mcg_validate_dense", "mcg_validate_sparse24", "mcg_validate_compress24",
            "mcg_dense_path", "mcg_dense_splits", "mcg_sparse24_path", "mcg_mfma_eval", "mcg_mfma_eval_k",
-           "mcg_mfma_probe")
+           "mcg_mfma_probe",
+           "rmsnorm_quant", "rmsnorm_backward", "mcg_rmsnorm_backward_workspace_bytes", "quantize_rows",
+           "dequantize_rows", "gemm_i8_scaled", "mcg_i8_scaled_workspace_bytes", "gemm_grad_i8",
+           "mcg_grad_i8_workspace_bytes", "mcg_validate_rmsnorm_quant", "mcg_validate_rmsnorm_backward",
+           "mcg_validate_quantize_rows", "mcg_validate_dequantize_rows", "mcg_validate_i8_scaled",
+           "mcg_validate_grad_i8")
 
 
 class MCGError(RuntimeError):
@@ -83,6 +88,27 @@ _lib.mcg_sparse24_path.argtypes = [_i32, _i32, _i64, _i64, _i64, _vp, _i64, _vp,
 _lib.mcg_mfma_eval.argtypes = [_i32, _i32, _i64, _vp, _vp, _vp, _vp, _vp]
 _lib.mcg_mfma_eval_k.argtypes = [_i32, _i32]
 _lib.mcg_mfma_probe.argtypes = [_i32, _i32, _i32, _vp, _vp, _vp, _i64, _i32, _vp, _vp, _vp]
+_lib.rmsnorm_quant.argtypes = [_i32, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _dbl, _vp, _i64, _vp, _i64, _vp, _vp, _vp]
+_lib.mcg_validate_rmsnorm_quant.argtypes = _lib.rmsnorm_quant.argtypes[:-1]
+_lib.rmsnorm_backward.argtypes = [_i32, _i32, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64,
+                                  _vp, _vp, _i64, _vp]
+_lib.mcg_validate_rmsnorm_backward.argtypes = _lib.rmsnorm_backward.argtypes[:-1]
+_lib.mcg_rmsnorm_backward_workspace_bytes.argtypes = [_i64, _i64]
+_lib.mcg_rmsnorm_backward_workspace_bytes.restype = _i64
+_lib.quantize_rows.argtypes = [_i32, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp]
+_lib.mcg_validate_quantize_rows.argtypes = _lib.quantize_rows.argtypes[:-1]
+_lib.dequantize_rows.argtypes = [_i32, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp]
+_lib.mcg_validate_dequantize_rows.argtypes = _lib.dequantize_rows.argtypes[:-1]
+_lib.gemm_i8_scaled.argtypes = [_i32, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _vp, _i64,
+                                _vp]
+_lib.mcg_validate_i8_scaled.argtypes = _lib.gemm_i8_scaled.argtypes[:-1]
+_lib.mcg_i8_scaled_workspace_bytes.argtypes = [_i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64]
+_lib.mcg_i8_scaled_workspace_bytes.restype = _i64
+_lib.gemm_grad_i8.argtypes = [_i32, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _dbl, _vp,
+                              _i64, _vp]
+_lib.mcg_validate_grad_i8.argtypes = _lib.gemm_grad_i8.argtypes[:-1]
+_lib.mcg_grad_i8_workspace_bytes.argtypes = [_i32, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i32]
+_lib.mcg_grad_i8_workspace_bytes.restype = _i64
 
 
 def lib():
@@ -282,3 +308,111 @@ def mfma_probe(dtypeA, dtypeB, sparse, a, b, idx, instr_per_wave, num_wg, sink, 
     _check("mcg_mfma_probe", _lib.mcg_mfma_probe(_dt(dtypeA), _dt(dtypeB), int(sparse), _ptr(a), _ptr(b),
                                                  _ptr(idx), int(instr_per_wave), int(num_wg), _ptr(sink),
                                                  _ptr(clocks), _stream(stream)))
+
+
+def _workspace(workspace, workspace_bytes):
+    """Address and size of a workspace (a tensor's own size when none is given)."""
+    if isinstance(workspace, torch.Tensor) and not workspace_bytes:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    return _ptr(workspace), int(workspace_bytes)
+
+
+def rmsnorm_quant(dtype, M, N, X, ldx, R, ldr, weight, eps, H, ldh, Q, ldq, scale, rstd=None, stream=None) -> None:
+    """Root-mean-square norm of X + R in 8 bits: codes Q with a scale per row; H
+    receives the sum and rstd the norms' factors (each may be None)."""
+    _check("rmsnorm_quant", _lib.rmsnorm_quant(
+        _dt(dtype), M, N, _ptr(X), ldx, _ptr(R), ldr, _ptr(weight), float(eps), _ptr(H), ldh, _ptr(Q), ldq,
+        _ptr(scale), _ptr(rstd), _stream(stream)))
+
+
+def rmsnorm_backward(dtype, dtypeX, M, N, dY, lddy, X, ldx, scaleX, weight, rstd, dR, lddr, dX, lddx, dW,
+                     workspace=None, workspace_bytes=0, stream=None) -> None:
+    """Gradient of the norm: dX (with dR added) and dW, from X in dtype or as 8-bit
+    codes with scaleX.  dW needs rmsnorm_backward_workspace_bytes(M, N) of workspace."""
+    ws, nb = _workspace(workspace, workspace_bytes)
+    _check("rmsnorm_backward", _lib.rmsnorm_backward(
+        _dt(dtype), _dt(dtypeX), M, N, _ptr(dY), lddy, _ptr(X), ldx, _ptr(scaleX), _ptr(weight), _ptr(rstd),
+        _ptr(dR), lddr, _ptr(dX), lddx, _ptr(dW), ws, nb, _stream(stream)))
+
+
+def rmsnorm_backward_workspace_bytes(M, N) -> int:
+    """Workspace bytes rmsnorm_backward needs for dW."""
+    return _lib.mcg_rmsnorm_backward_workspace_bytes(M, N)
+
+
+def quantize_rows(dtype, M, N, X, ldx, Q, ldq, scale, stream=None) -> None:
+    """The rows of X as 8-bit codes with a scale each."""
+    _check("quantize_rows", _lib.quantize_rows(_dt(dtype), M, N, _ptr(X), ldx, _ptr(Q), ldq, _ptr(scale),
+                                               _stream(stream)))
+
+
+def dequantize_rows(dtypeD, M, N, Q, ldq, scale, D, ldd, stream=None) -> None:
+    """The values of 8-bit rows, rounded once to dtypeD."""
+    _check("dequantize_rows", _lib.dequantize_rows(_dt(dtypeD), M, N, _ptr(Q), ldq, _ptr(scale), _ptr(D), ldd,
+                                                   _stream(stream)))
+
+
+def gemm_i8_scaled(layoutB, M, N, K, A, lda, scaleA, B, ldb, scaleB, bias, D, ldd, dtypeD, workspace=None,
+                   workspace_bytes=0, stream=None) -> None:
+    """D = scaleA[i] * scaleB[j] * (A . B) + bias[j] on int8 operands; a workspace
+    (up to i8_scaled_workspace_bytes) lets few-tile products cut K."""
+    ws, nb = _workspace(workspace, workspace_bytes)
+    _check("gemm_i8_scaled", _lib.gemm_i8_scaled(
+        _lay(layoutB), M, N, K, _ptr(A), lda, _ptr(scaleA), _ptr(B), ldb, _ptr(scaleB), _ptr(bias), _ptr(D), ldd,
+        _dt(dtypeD), ws, nb, _stream(stream)))
+
+
+def i8_scaled_workspace_bytes(layoutB, M, N, K, A, lda, B, ldb) -> int:
+    """Workspace bytes gemm_i8_scaled can use for these operands."""
+    return _lib.mcg_i8_scaled_workspace_bytes(_lay(layoutB), M, N, K, _ptr(A), lda, _ptr(B), ldb)
+
+
+def gemm_grad_i8(dtypeA, layoutA, M, N, K, A, lda, Q, ldq, scaleK, C, D, ldd, dtypeD, beta=0.0, workspace=None,
+                 workspace_bytes=0, stream=None) -> None:
+    """D = A . (scaleK[k] * Q[k]) + beta * C, A 16-bit and Q int8 rows: the weight
+    gradient from an 8-bit checkpoint, or the input gradient from 8-bit weights."""
+    ws, nb = _workspace(workspace, workspace_bytes)
+    _check("gemm_grad_i8", _lib.gemm_grad_i8(
+        _dt(dtypeA), _lay(layoutA), M, N, K, _ptr(A), lda, _ptr(Q), ldq, _ptr(scaleK), _ptr(C), _ptr(D), ldd,
+        _dt(dtypeD), float(beta), ws, nb, _stream(stream)))
+
+
+def grad_i8_workspace_bytes(dtypeA, layoutA, M, N, K, A, lda, Q, ldq, dtypeD) -> int:
+    """Workspace bytes gemm_grad_i8 can use for these operands."""
+    return _lib.mcg_grad_i8_workspace_bytes(_dt(dtypeA), _lay(layoutA), M, N, K, _ptr(A), lda, _ptr(Q), ldq,
+                                            _dt(dtypeD))
+
+
+def validate_rmsnorm_quant(dtype, M, N, X, ldx, R, ldr, weight, eps, H, ldh, Q, ldq, scale, rstd=None) -> int:
+    return _lib.mcg_validate_rmsnorm_quant(_dt(dtype), M, N, _ptr(X), ldx, _ptr(R), ldr, _ptr(weight), float(eps),
+                                           _ptr(H), ldh, _ptr(Q), ldq, _ptr(scale), _ptr(rstd))
+
+
+def validate_rmsnorm_backward(dtype, dtypeX, M, N, dY, lddy, X, ldx, scaleX, weight, rstd, dR, lddr, dX, lddx, dW,
+                              workspace=None, workspace_bytes=0) -> int:
+    ws, nb = _workspace(workspace, workspace_bytes)
+    return _lib.mcg_validate_rmsnorm_backward(_dt(dtype), _dt(dtypeX), M, N, _ptr(dY), lddy, _ptr(X), ldx,
+                                              _ptr(scaleX), _ptr(weight), _ptr(rstd), _ptr(dR), lddr, _ptr(dX), lddx,
+                                              _ptr(dW), ws, nb)
+
+
+def validate_quantize_rows(dtype, M, N, X, ldx, Q, ldq, scale) -> int:
+    return _lib.mcg_validate_quantize_rows(_dt(dtype), M, N, _ptr(X), ldx, _ptr(Q), ldq, _ptr(scale))
+
+
+def validate_dequantize_rows(dtypeD, M, N, Q, ldq, scale, D, ldd) -> int:
+    return _lib.mcg_validate_dequantize_rows(_dt(dtypeD), M, N, _ptr(Q), ldq, _ptr(scale), _ptr(D), ldd)
+
+
+def validate_i8_scaled(layoutB, M, N, K, A, lda, scaleA, B, ldb, scaleB, bias, D, ldd, dtypeD, workspace=None,
+                       workspace_bytes=0) -> int:
+    ws, nb = _workspace(workspace, workspace_bytes)
+    return _lib.mcg_validate_i8_scaled(_lay(layoutB), M, N, K, _ptr(A), lda, _ptr(scaleA), _ptr(B), ldb, _ptr(scaleB),
+                                       _ptr(bias), _ptr(D), ldd, _dt(dtypeD), ws, nb)
+
+
+def validate_grad_i8(dtypeA, layoutA, M, N, K, A, lda, Q, ldq, scaleK, C, D, ldd, dtypeD, beta=0.0, workspace=None,
+                     workspace_bytes=0) -> int:
+    ws, nb = _workspace(workspace, workspace_bytes)
+    return _lib.mcg_validate_grad_i8(_dt(dtypeA), _lay(layoutA), M, N, K, _ptr(A), lda, _ptr(Q), ldq, _ptr(scaleK),
+                                     _ptr(C), _ptr(D), ldd, _dt(dtypeD), float(beta), ws, nb)

@@ -17,8 +17,11 @@ LIB = os.path.join(HERE, "_libmcg.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["gemm_dense.hip", "gemm_skinny_n.hip", "gemm_skinny_m.hip", "gemm_stream.hip", "gemm_fast.hip", "gemm_fast_mid.hip", "gemm_fast_sk.hip", "gemm_fast_mid_sk.hip", "gemm_sparse.hip",
-           "gemm_sparse_fast.hip", "gemm_f64.hip", "numerics.hip", "mfma_probe.hip", "api.cpp"]
-HEADERS = ["arch_gfx950.hpp", "frag_layout.hpp", "tile_io.hpp", "fast_tiles.hpp", "tile_order.hpp", "gemm_fast_kernel.hpp", "gemm_kernels.hpp", "dense_general.hpp", "sparse_ops.hpp"]
+           "gemm_sparse_fast.hip", "gemm_f64.hip", "numerics.hip", "mfma_probe.hip",
+           "rows_quant.hip", "rmsnorm_backward.hip", "gemm_i8_scaled.hip", "gemm_grad_i8.hip",
+           "api.cpp", "api_linear8.cpp"]
+HEADERS = ["arch_gfx950.hpp", "frag_layout.hpp", "tile_io.hpp", "fast_tiles.hpp", "tile_order.hpp", "gemm_fast_kernel.hpp", "gemm_kernels.hpp", "dense_general.hpp", "sparse_ops.hpp",
+           "api_util.hpp", "linear8.hpp", "row_vec.hpp", "tile_any.hpp"]
 
 # Packed fp32 VALU forms are disabled for all device code (hipcc's host pass
 # reports the feature as unknown, which is harmless).

@@ -6,7 +6,10 @@
 #include <cstring>
 
 #include "../../include/mcg.h"
+#include "api_util.hpp"
 #include "gemm_kernels.hpp"
+
+using namespace mcg::host;
 
 namespace {
 
@@ -18,23 +21,7 @@ bool is_in_dtype(int dt) { return dt >= MCG_BF16 && dt <= MCG_FP8_E5M2; }
 static int out_format(int dtypeD) {
   return dtypeD == MCG_BF16 ? mcg::OUT_BF16 : dtypeD == MCG_F16 ? mcg::OUT_F16 : mcg::OUT_32;
 }
-static bool float_out(int dtypeD) { return dtypeD == MCG_F32 || dtypeD == MCG_BF16 || dtypeD == MCG_F16; }
 
-int elem_bytes(int dt) {
-  switch (dt) {
-    case MCG_BF16:
-    case MCG_F16: return 2;
-    case MCG_I8:
-    case MCG_FP8_E4M3:
-    case MCG_FP8_E5M2: return 1;
-    case MCG_F32:
-    case MCG_I32: return 4;
-    case MCG_F64: return 8;
-    default: return 0;
-  }
-}
-bool aligned_to(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
-bool valid_layout(int l) { return l == MCG_K_CONTIG || l == MCG_MN_CONTIG; }
 bool int32_integral(double v) {
   return std::isfinite(v) && v == std::floor(v) && v >= -2147483648.0 && v <= 2147483647.0;
 }
@@ -55,6 +42,11 @@ int probe_device(int dev) {
   g_arch_state[dev].store(std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : 2, std::memory_order_relaxed);
   return MCG_SUCCESS;
 }
+
+}  // namespace
+
+namespace mcg {
+namespace host {
 
 int check_arch() {
   int dev = 0;
@@ -77,10 +69,13 @@ int current_num_cu() {
   return g_num_cu[dev].load(std::memory_order_relaxed);
 }
 
+}  // namespace host
+}  // namespace mcg
+
+namespace {
+
 // A float alpha/beta the kernels receive as fp32 must stay finite there.
 bool finite_as_f32(double v) { return std::isfinite((float)v); }
-
-int hip_status(hipError_t e) { return e == hipSuccess ? MCG_SUCCESS : MCG_ERR_HIP; }
 
 }  // namespace
 

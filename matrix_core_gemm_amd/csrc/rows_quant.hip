@@ -1,0 +1,254 @@
+// rows_quant.hip -- rows of a matrix to 8 bits with one scale each, after the
+// root-mean-square norm (rmsnorm_quant) or as they are (quantize_rows), and back
+// (dequantize_rows).
+//
+//   h = x + r,  rstd = (mean(h^2) + eps)^(-1/2),  y = h * w * rstd
+//   scale = max|y| / 127,  q = rint(y / scale)
+//
+// rstd > 0 is common to the row, so max|y| = rstd * max|h w| and y / scale =
+// 127 h w / max|h w|: both reductions (the sum of squares and the largest
+// |h w|) run over the same values at once, and the codes need no rstd.  A row is
+// read once and kept in registers between its reductions and its stores.
+// Statistics and products are binary32; h is rounded once, to be stored, and the
+// norm is taken of the unrounded sum.
+//
+// Bound: memory (7 bytes per element with a 16-bit residual, 3 without).
+#include "row_vec.hpp"
+
+namespace mcg {
+namespace rows {
+
+constexpr float QMAX = 127.0f;
+constexpr int64_t MAX_BLOCKS = 1 << 20;  // workgroups along the rows (a launch holds less than 2^32 threads)
+
+// Sum and largest pattern over the TPR threads of a row, in all of them.
+template <int TPR>
+__device__ __forceinline__ void row_reduce(float& ss, uint32_t& top, int phase) {
+  ss = wave_sum(ss);
+  top = wave_umax(top);
+  if constexpr (TPR > 64) {
+    constexpr int NWV = TPR / 64;
+    __shared__ float ls[2][NWV];  // by turns: a wavefront may be one row ahead
+    __shared__ uint32_t lt[2][NWV];
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+      ls[phase][wave] = ss;
+      lt[phase][wave] = top;
+    }
+    __syncthreads();
+    ss = ls[phase][0];
+    top = lt[phase][0];
+#pragma unroll
+    for (int i = 1; i < NWV; ++i) {
+      ss += ls[phase][i];
+      top = top > lt[phase][i] ? top : lt[phase][i];
+    }
+  }
+}
+
+// A row's statistics from its reductions: the factor of its codes (after the
+// exact factor pre, which keeps 127 / max in range for a row of tiny values),
+// its scale and rstd.  A row with a NaN or an infinity, or whose squares
+// overflow, gets the scale NaN and codes 0; a row of zeros the scale 0.
+struct RowStat {
+  float pre, inv, scale, rstd;
+};
+template <bool NORM>
+__device__ __forceinline__ RowStat row_stat(float ss, uint32_t top, int64_t n, float eps) {
+  RowStat s;
+  const float t = bit_cast<float>(top);
+  s.rstd = 1.0f;
+  if constexpr (NORM) s.rstd = 1.0f / __builtin_sqrtf((n > 0 ? ss / (float)n : 0.0f) + eps);
+  const bool finite = top < 0x7f800000u && (!NORM || ss < __builtin_inff());
+  s.pre = t < 0x1p-100f ? 0x1p100f : 1.0f;
+  s.inv = finite && t > 0.0f ? QMAX / (t * s.pre) : 0.0f;
+  if (!finite) s.scale = __builtin_nanf("");
+  else s.scale = t > 0.0f ? t * s.rstd / QMAX : 0.0f;
+  return s;
+}
+
+// Codes of eight values: nearest even, at most 127 in magnitude (127 * t / t may
+// round past it by one unit).  inv == 0 (see RowStat) gives zeros.
+__device__ __forceinline__ Raw8<DT_I8> codes8(const float (&y)[8], const RowStat& s) {
+  Raw8<DT_I8> v;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v.w[i] = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float c = __builtin_rintf(fminf(fmaxf(y[4 * i + e] * s.pre * s.inv, -QMAX), QMAX));
+      v.w[i] |= ((uint32_t)(int)(s.inv == 0.0f ? 0.0f : c) & 0xffu) << (8 * e);
+    }
+  }
+  return v;
+}
+
+// One vector of a row: h (widened sum) and its products with the weights.
+template <int DT, bool NORM>
+__device__ __forceinline__ void load_h(const RowsQuantArgs& p, const char* x, const char* r, int64_t c, float (&h)[8]) {
+  widen8<DT>(load8<DT>(x, c, p.N), h);
+  if (NORM && r) {
+    float y[8];
+    widen8<DT>(load8<DT>(r, c, p.N), y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] += y[e];
+  }
+}
+template <int DT, bool NORM>
+__device__ __forceinline__ void weigh(const RowsQuantArgs& p, int64_t c, float (&h)[8]) {
+  if (NORM && p.W) {
+    float w[8];
+    widen8<DT>(load8<DT>(p.W, c, p.N), w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] *= w[e];
+  }
+}
+__device__ __forceinline__ void stat8(const float (&h)[8], float& ss) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(h[e], h[e], ss);
+}
+__device__ __forceinline__ void top8(const float (&y)[8], uint32_t& top) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t b = bit_cast<uint32_t>(y[e]) & 0x7fffffffu;
+    top = top > b ? top : b;
+  }
+}
+
+// TPR threads per row (a wavefront or a workgroup), NV vectors of eight elements
+// per thread: rows of up to 8 * TPR * NV elements.
+template <int DT, bool NORM, int TPR, int NV>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rows_quant_kernel(RowsQuantArgs p) {
+  constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
+  constexpr int ES = elem_size<DT>();
+  const int t = threadIdx.x % TPR;
+  int phase = 0;
+  // whole wavefronts leave the loop together, whole workgroups where a row is a workgroup's
+  for (int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / TPR; row < p.M;
+       row += (int64_t)gridDim.x * RPW, phase ^= 1) {
+    const char* x = p.X + row * p.ldx * ES;
+    const char* r = p.R ? p.R + row * p.ldr * ES : nullptr;
+    float y[NV][8];
+    float ss = 0.0f;
+    uint32_t top = 0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) load_h<DT, NORM>(p, x, r, (int64_t)(v * TPR + t) * 8, y[v]);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int64_t c = (int64_t)(v * TPR + t) * 8;
+      if constexpr (NORM) {
+        if (p.H) store8<DT>(p.H + row * p.ldh * ES, c, p.N, narrow8<DT>(y[v]));
+        stat8(y[v], ss);
+        weigh<DT, NORM>(p, c, y[v]);
+      }
+      top8(y[v], top);
+    }
+    row_reduce<TPR>(ss, top, phase);
+    const RowStat s = row_stat<NORM>(ss, top, p.N, p.eps);
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+      store8<DT_I8>((char*)p.Q + row * p.ldq, (int64_t)(v * TPR + t) * 8, p.N, codes8(y[v], s));
+    if (t == 0) {
+      p.scale[row] = s.scale;
+      if (NORM && p.rstd) p.rstd[row] = s.rstd;
+    }
+  }
+}
+
+// Rows of any length: the row is read a second time (through the caches) for its
+// codes.  H is written in the second pass, by the thread that has just read the
+// same elements of X and R, so it may be either of them.
+template <int DT, bool NORM>
+__global__ __launch_bounds__(1024) void rows_quant_long_kernel(RowsQuantArgs p) {
+  constexpr int ES = elem_size<DT>();
+  int phase = 0;
+  for (int64_t row = blockIdx.x; row < p.M; row += gridDim.x, phase ^= 1) {
+    const char* x = p.X + row * p.ldx * ES;
+    const char* r = p.R ? p.R + row * p.ldr * ES : nullptr;
+    float ss = 0.0f;
+    uint32_t top = 0;
+    for (int64_t c = (int64_t)threadIdx.x * 8; c < p.N; c += 8192) {
+      float h[8];
+      load_h<DT, NORM>(p, x, r, c, h);
+      if constexpr (NORM) {
+        stat8(h, ss);
+        weigh<DT, NORM>(p, c, h);
+      }
+      top8(h, top);
+    }
+    row_reduce<1024>(ss, top, phase);
+    const RowStat s = row_stat<NORM>(ss, top, p.N, p.eps);
+    for (int64_t c = (int64_t)threadIdx.x * 8; c < p.N; c += 8192) {
+      float h[8];
+      load_h<DT, NORM>(p, x, r, c, h);
+      if constexpr (NORM) {
+        if (p.H) store8<DT>(p.H + row * p.ldh * ES, c, p.N, narrow8<DT>(h));
+        weigh<DT, NORM>(p, c, h);
+      }
+      store8<DT_I8>((char*)p.Q + row * p.ldq, c, p.N, codes8(h, s));
+    }
+    if (threadIdx.x == 0) {
+      p.scale[row] = s.scale;
+      if (NORM && p.rstd) p.rstd[row] = s.rstd;
+    }
+  }
+}
+
+// The values of 8-bit rows: one vector of eight codes per thread, columns along x.
+template <int DT>
+__global__ __launch_bounds__(256) void rows_dequant_kernel(RowsDequantArgs p) {
+  const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+  if (c >= p.N) return;
+  for (int64_t row = blockIdx.y; row < p.M; row += gridDim.y) {
+    float x[8];
+    widen8<DT_I8>(load8<DT_I8>((const char*)p.Q + row * p.ldq, c, p.N), x);
+    const float s = p.scale[row];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] *= s;
+    store8<DT>(p.D + row * p.ldd * elem_size<DT>(), c, p.N, narrow8<DT>(x));
+  }
+}
+
+template <int DT, bool NORM, int TPR, int NV>
+static hipError_t launch_one(const RowsQuantArgs& a, hipStream_t s) {
+  constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
+  const int64_t blocks = min((a.M + RPW - 1) / RPW, MAX_BLOCKS);
+  hipLaunchKernelGGL((rows_quant_kernel<DT, NORM, TPR, NV>), dim3((unsigned)blocks), dim3(RPW * TPR), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int DT, bool NORM>
+static hipError_t launch_dt(const RowsQuantArgs& a, int num_cu, hipStream_t s) {
+  const int64_t n = a.N;
+  if (n <= 512) return launch_one<DT, NORM, 64, 1>(a, s);
+  if (n <= 1024) return launch_one<DT, NORM, 64, 2>(a, s);
+  if (n <= 2048) return launch_one<DT, NORM, 256, 1>(a, s);
+  if (n <= 4096) return launch_one<DT, NORM, 256, 2>(a, s);
+  if (n <= 8192) return a.M <= num_cu ? launch_one<DT, NORM, 1024, 1>(a, s) : launch_one<DT, NORM, 256, 4>(a, s);
+  if (n <= 16384) return launch_one<DT, NORM, 1024, 2>(a, s);
+  hipLaunchKernelGGL((rows_quant_long_kernel<DT, NORM>), dim3((unsigned)min(a.M, MAX_BLOCKS)), dim3(1024), 0, s, a);
+  return hipGetLastError();
+}
+
+template <bool NORM>
+static hipError_t launch_norm(int dt, const RowsQuantArgs& a, int num_cu, hipStream_t s) {
+  if (dt == DT_BF16) return launch_dt<DT_BF16, NORM>(a, num_cu, s);
+  if (dt == DT_F16) return launch_dt<DT_F16, NORM>(a, num_cu, s);
+  return launch_dt<DT_F32, NORM>(a, num_cu, s);
+}
+
+}  // namespace rows
+
+hipError_t launch_rows_quant(int dt, bool norm, const RowsQuantArgs& a, int num_cu, hipStream_t s) {
+  return norm ? rows::launch_norm<true>(dt, a, num_cu, s) : rows::launch_norm<false>(dt, a, num_cu, s);
+}
+
+hipError_t launch_rows_dequant(int dt, const RowsDequantArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)((a.N + 2047) / 2048), (unsigned)(a.M < 65535 ? a.M : 65535));
+  if (dt == DT_BF16) hipLaunchKernelGGL((rows::rows_dequant_kernel<DT_BF16>), grid, dim3(256), 0, s, a);
+  else if (dt == DT_F16) hipLaunchKernelGGL((rows::rows_dequant_kernel<DT_F16>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((rows::rows_dequant_kernel<rows::DT_F32>), grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace mcg
