@@ -135,8 +135,15 @@ def _ptr(t):
     return int(t)
 
 
+# The current stream's handle without a torch.cuda.Stream object around it: 0.2 us
+# instead of 2.8 us, of 7 us for a whole call of a small operator.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream

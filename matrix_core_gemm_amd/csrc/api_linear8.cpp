@@ -134,7 +134,7 @@ int mcg_validate_rmsnorm_backward(int dtype, int dtypeX, int64_t M, int64_t N, c
 }
 
 int64_t mcg_rmsnorm_backward_workspace_bytes(int64_t M, int64_t N) {
-  return M <= 0 || N <= 0 ? 0 : mcg::norm_grad_parts(M, N) * N * 4;
+  return M <= 0 || N <= 0 ? 0 : mcg::norm_grad_workspace(M, N);
 }
 
 int rmsnorm_backward(int dtype, int dtypeX, int64_t M, int64_t N, const void* dY, int64_t lddy, const void* X,

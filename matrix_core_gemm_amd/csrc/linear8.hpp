@@ -39,11 +39,11 @@ struct NormGradArgs {
   const char* dR;       // or null
   char* dX;
   float* dW;            // or null
-  float* part;          // workspace: partial rows of dW (norm_grad_parts(M, N) x N)
+  float* part;          // workspace of norm_grad_workspace(M, N) bytes: partial rows of dW
   int64_t M, N, lddy, ldx, lddr, lddx;
   int64_t parts;        // filled by the launcher
 };
-int64_t norm_grad_parts(int64_t M, int64_t N);
+int64_t norm_grad_workspace(int64_t M, int64_t N);
 hipError_t launch_norm_grad(int dt, bool x8, const NormGradArgs& a, hipStream_t s);
 
 // D = (A . B) * sa_i * sb_j + bias_j, int8 operands (gemm_i8_scaled.hip).

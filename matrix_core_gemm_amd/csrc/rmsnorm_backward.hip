@@ -13,14 +13,19 @@
 // the partial rows in a fixed order (no atomics: the result does not depend on
 // timing).  Everything is summed in binary32.
 //
-// Bound: memory (8 bytes per element with 16-bit x and dr).
+// Bound: memory (8 bytes per element with 16-bit x and dr).  8192 x 4096 bf16: 55 us
+// (4.9 TB/s), of which the sum of the partial rows takes 4; with 1024 partial rows,
+// summed by 8 threads a column one element at a time, and no loads ahead 87 us.
 #include "row_vec.hpp"
 
 namespace mcg {
 namespace rows {
 
-constexpr int64_t MAX_PARTS = 1024;  // partial rows of dw
+constexpr int64_t MAX_PARTS = 512;   // partial rows of dw: workgroups of the row kernels
 constexpr int64_t MAX_BLOCKS = 1 << 20;  // workgroups along the rows (a launch holds less than 2^32 threads)
+
+// Elements between the partial rows: whole 16-byte vectors.
+__host__ __device__ inline int64_t part_stride(int64_t n) { return (n + 3) & ~(int64_t)3; }
 
 template <int TPR>
 __device__ __forceinline__ float row_sum(float x, int phase) {
@@ -64,54 +69,98 @@ __device__ __forceinline__ void store_dx(const NormGradArgs& p, int64_t row, int
   store8<DT>(p.dX + row * p.lddx * ES, c, p.N, narrow8<DT>(d));
 }
 
-template <int DT, int DTX, int TPR, int NV>
+// One row per TPR threads, NV vectors of eight elements per thread; a workgroup
+// walks the rows a grid apart, the next row's loads in flight while it reduces this
+// one (dX may be dY or dR, so that the compiler itself would keep them behind the
+// stores), and leaves one partial row of dw.  WHOLE: rows of whole vectors.
+template <int DT, int DTX, int TPR, int NV, bool WHOLE>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(NormGradArgs p) {
   constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
   constexpr int ES = elem_size<DT>();
-  const int t = threadIdx.x % TPR;
-  const int64_t first = (int64_t)blockIdx.x * RPW + threadIdx.x / TPR;
-  if (first >= p.parts) return;  // whole wavefronts, and only where a row is one wavefront
-  float w[NV][8], dw[NV][8];
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    if (p.W) {
-      widen8<DT>(load8<DT>(p.W, (int64_t)(v * TPR + t) * 8, p.N), w[v]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[v][e] = 1.0f;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) dw[v][e] = 0.0f;
-  }
-  int phase = 0;
-  for (int64_t row = first; row < p.M; row += p.parts, phase ^= 1) {
-    const float rstd = p.rstd[row];
-    float g[NV][8], x[NV][8];
-    float sum = 0.0f;
+  const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const int64_t step = (int64_t)gridDim.x * RPW;
+  float dw[NV][8];
+  Raw8<DT> w[NV], dy[NV], dr[NV];
+  Raw8<DTX> xr[NV];
+  float rstd = 0.0f, xs = 1.0f;
+  auto load_row = [&](int64_t m) {
+    rstd = p.rstd[m];
+    if constexpr (DTX == DT_I8) xs = p.xscale[m];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int64_t c = (int64_t)(v * TPR + t) * 8;
-      load_x<DT, DTX>(p, row, c, x[v]);
-      widen8<DT>(load8<DT>(p.dY + row * p.lddy * ES, c, p.N), g[v]);
+      dy[v] = load8<DT, WHOLE>(p.dY + m * p.lddy * ES, c, p.N);
+      xr[v] = load8<DTX, WHOLE>(p.X + m * p.ldx * elem_size<DTX>(), c, p.N);
+      if (p.dR) dr[v] = load8<DT, WHOLE>(p.dR + m * p.lddr * ES, c, p.N);
     }
+  };
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    if (p.W) w[v] = load8<DT, WHOLE>(p.W, (int64_t)(v * TPR + t) * 8, p.N);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[v][e] = 0.0f;
+  }
+  int64_t row = (int64_t)blockIdx.x * RPW + sub;
+  if (row < p.M) load_row(row);
+  for (int phase = 0; row < p.M; row += step, phase ^= 1) {
+    const float rs = rstd;
+    float g[NV][8], x[NV][8], d[NV][8];
+    float sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      widen8<DT>(dy[v], g[v]);
+      widen8<DTX>(xr[v], x[v]);
+      if (p.dR) widen8<DT>(dr[v], d[v]);
+      if constexpr (DTX == DT_I8) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[v][e] *= xs;
+      }
+    }
+    if (row + step < p.M) load_row(row + step);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float wv[8];
+      if (p.W) widen8<DT>(w[v], wv);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        dw[v][e] = __builtin_fmaf(g[v][e] * rs, x[v][e], dw[v][e]);
+        if (p.W) g[v][e] *= wv[e];
+        sum = __builtin_fmaf(g[v][e], x[v][e], sum);
+      }
+    }
+    sum = row_sum<TPR>(sum, phase);
+    const float k = sum * (rs * rs) / (float)p.N;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        o[e] = rs * __builtin_fmaf(-k, x[v][e], g[v][e]);
+        if (p.dR) o[e] += d[v][e];
+      }
+      store8<DT, WHOLE>(p.dX + row * p.lddx * ES, (int64_t)(v * TPR + t) * 8, p.N, narrow8<DT>(o));
+    }
+  }
+  if (!p.dW) return;
+  if constexpr (RPW > 1) {
+    // the workgroup's wavefronts each hold rows of their own: one partial row of them
+    __shared__ float acc[RPW][TPR * NV * 8];
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        dw[v][e] = __builtin_fmaf(g[v][e] * rstd, x[v][e], dw[v][e]);
-        g[v][e] *= w[v][e];
-        sum = __builtin_fmaf(g[v][e], x[v][e], sum);
-      }
-    sum = row_sum<TPR>(sum, phase);
-    const float k = sum * (rstd * rstd) / (float)p.N;
+      for (int e = 0; e < 8; ++e) acc[sub][(v * 8 + e) * TPR + t] = dw[v][e];
+    __syncthreads();
+    if (sub > 0) return;
 #pragma unroll
-    for (int v = 0; v < NV; ++v) store_dx<DT>(p, row, (int64_t)(v * TPR + t) * 8, rstd, k, g[v], x[v]);
-  }
-  if (p.dW) {
-    char* part = (char*)(p.part + first * p.N);
+    for (int v = 0; v < NV; ++v)
 #pragma unroll
-    for (int v = 0; v < NV; ++v) store8<DT_F32>(part, (int64_t)(v * TPR + t) * 8, p.N, narrow8<DT_F32>(dw[v]));
+      for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int i = 1; i < RPW; ++i) dw[v][e] += acc[i][(v * 8 + e) * TPR + t];
   }
+  char* part = (char*)(p.part + blockIdx.x * part_stride(p.N));
+#pragma unroll
+  for (int v = 0; v < NV; ++v) store8<DT_F32, WHOLE>(part, (int64_t)(v * TPR + t) * 8, p.N, narrow8<DT_F32>(dw[v]));
 }
 
 // Rows of any length: dx with the row read twice, and dw's partial rows column by
@@ -161,32 +210,51 @@ __global__ __launch_bounds__(256) void norm_grad_long_dw_kernel(NormGradArgs p) 
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[e] = __builtin_fmaf(g[e] * rstd, x[e], dw[e]);
   }
-  store8<DT_F32>((char*)(p.part + (int64_t)blockIdx.y * p.N), c, p.N, narrow8<DT_F32>(dw));
+  store8<DT_F32>((char*)(p.part + (int64_t)blockIdx.y * part_stride(p.N)), c, p.N, narrow8<DT_F32>(dw));
 }
 
-// dw = sum of the partial rows, 32 columns per workgroup: 8 threads of a column
-// take every eighth part, and their sums are added in order through LDS.
+// dw = sum of the partial rows, 32 columns (one 128-byte line of a row) per
+// workgroup: 32 groups of 8 threads take every 32nd part, SUM_BATCH loads in
+// flight, and the groups' sums are added in order through LDS.
+constexpr int SUM_BATCH = 8;
 __global__ __launch_bounds__(256) void norm_grad_sum_kernel(NormGradArgs p) {
-  const int col = threadIdx.x & 31, sub = threadIdx.x >> 5;
-  const int64_t n = (int64_t)blockIdx.x * 32 + col;
-  __shared__ float ls[8][32];
-  float s = 0.0f;
-  if (n < p.N)
-    for (int64_t g = sub; g < p.parts; g += 8) s += p.part[g * p.N + n];
-  ls[sub][col] = s;
-  __syncthreads();
-  if (sub == 0 && n < p.N) {
+  const int c4 = threadIdx.x & 7, sub = threadIdx.x >> 3;
+  const int64_t n = (int64_t)blockIdx.x * 32 + 4 * c4, stride = part_stride(p.N);
+  __shared__ float ls[32][33];
+  float s[4] = {0, 0, 0, 0};
+  if (n < p.N) {
+    const float* src = p.part + n;  // 16-byte aligned; past N the row's padding
+    for (int64_t g0 = sub; g0 < p.parts; g0 += 32 * SUM_BATCH) {
+      f32x4 v[SUM_BATCH];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += ls[i][col];
-    p.dW[n] = s;
+      for (int u = 0; u < SUM_BATCH; ++u) {
+        const int64_t g = g0 + 32 * u;
+        v[u] = g < p.parts ? *(const f32x4*)(src + g * stride) : f32x4{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int u = 0; u < SUM_BATCH; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += v[u][e];
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) ls[sub][4 * c4 + e] = s[e];
+  __syncthreads();
+  const int64_t col = (int64_t)blockIdx.x * 32 + threadIdx.x;
+  if (threadIdx.x < 32 && col < p.N) {
+    float d = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) d += ls[i][threadIdx.x];
+    p.dW[col] = d;
   }
 }
 
 template <int DT, int DTX, int TPR, int NV>
 static void launch_one(const NormGradArgs& a, hipStream_t s) {
   constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
-  const int64_t blocks = (a.parts + RPW - 1) / RPW;
-  hipLaunchKernelGGL((norm_grad_kernel<DT, DTX, TPR, NV>), dim3((unsigned)blocks), dim3(RPW * TPR), 0, s, a);
+  const dim3 grid((unsigned)a.parts), block(RPW * TPR);
+  if (a.N % 8 == 0) hipLaunchKernelGGL((norm_grad_kernel<DT, DTX, TPR, NV, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((norm_grad_kernel<DT, DTX, TPR, NV, false>), grid, block, 0, s, a);
 }
 
 template <int DT, int DTX>
@@ -216,7 +284,15 @@ static hipError_t launch_dt(const NormGradArgs& a, hipStream_t s) {
 
 }  // namespace rows
 
-int64_t norm_grad_parts(int64_t M, int64_t) { return M < rows::MAX_PARTS ? M : rows::MAX_PARTS; }
+// Rows of the kernel's workgroups: 4 wavefronts with a row each up to 1024 columns.
+int64_t norm_grad_parts(int64_t M, int64_t N) {
+  const int64_t groups = N <= 1024 ? (M + 3) / 4 : M;
+  return groups < rows::MAX_PARTS ? groups : rows::MAX_PARTS;
+}
+// (stated for one row per workgroup, whatever the kernel)
+int64_t norm_grad_workspace(int64_t M, int64_t N) {
+  return (M < rows::MAX_PARTS ? M : rows::MAX_PARTS) * rows::part_stride(N) * 4;
+}
 
 hipError_t launch_norm_grad(int dt, bool x8, const NormGradArgs& a0, hipStream_t s) {
   NormGradArgs a = a0;

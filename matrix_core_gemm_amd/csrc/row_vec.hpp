@@ -27,8 +27,10 @@ struct Raw8 {
   uint32_t w[DWORDS];
 };
 
-// Elements [c, c + 8) of a row of n elements; zeros past its end.
-template <int DT>
+// Elements [c, c + 8) of a row of n elements; zeros past its end.  WHOLE: n is a
+// multiple of 8 (the partial vector's code, 8 branches wherever it stands, costs the
+// row kernels scalar registers and time).
+template <int DT, bool WHOLE = false>
 __device__ __forceinline__ Raw8<DT> load8(const char* row, int64_t c, int64_t n) {
   constexpr int ES = elem_size<DT>();
   Raw8<DT> v;
@@ -40,6 +42,7 @@ __device__ __forceinline__ Raw8<DT> load8(const char* row, int64_t c, int64_t n)
   } else {
 #pragma unroll
     for (int i = 0; i < Raw8<DT>::DWORDS; ++i) v.w[i] = 0;
+    if constexpr (WHOLE) return v;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       if (c + e >= n) continue;
@@ -52,7 +55,7 @@ __device__ __forceinline__ Raw8<DT> load8(const char* row, int64_t c, int64_t n)
   return v;
 }
 
-template <int DT>
+template <int DT, bool WHOLE = false>
 __device__ __forceinline__ void store8(char* row, int64_t c, int64_t n, const Raw8<DT>& v) {
   constexpr int ES = elem_size<DT>();
   if (c + 8 <= n) {
@@ -61,7 +64,7 @@ __device__ __forceinline__ void store8(char* row, int64_t c, int64_t n, const Ra
 #pragma unroll
     for (int i = 0; i < Raw8<DT>::DWORDS; ++i) u.w[i] = v.w[i];
     *(U*)(row + c * ES) = u;
-  } else {
+  } else if constexpr (!WHOLE) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       if (c + e >= n) continue;
