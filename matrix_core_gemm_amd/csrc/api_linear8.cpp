@@ -35,9 +35,9 @@ mcg::ScaledArgs scaled_args(int64_t M, int64_t N, int64_t K, const void* A, int6
   a.K = K;
   a.lda = lda;
   a.ldb = ldb;
-  a.ldd = ldd;
+  a.ldc = ldd;
   a.out = out_format(dtypeD);
-  a.vec_d = aligned_to(D, 4 * elem_bytes(dtypeD)) && ldd % 4 == 0;
+  a.vec_cd = aligned_to(D, 4 * elem_bytes(dtypeD)) && ldd % 4 == 0;
   return a;
 }
 
@@ -257,9 +257,11 @@ int gemm_i8_scaled(int layoutB, int64_t M, int64_t N, int64_t K, const int8_t* A
   a.sa = scaleA;
   a.sb = scaleB;
   a.bias = bias;
-  a.ws = (int32_t*)workspace;
-  mcg::plan_scaled(a, layoutB, current_num_cu(), workspace ? workspace_bytes : 0);
-  return hip_status(mcg::launch_scaled(layoutB, a, (hipStream_t)stream));
+  a.ws = workspace;
+  a.ws_bytes = workspace ? workspace_bytes : 0;
+  const int num_cu = current_num_cu();
+  mcg::plan_scaled(a, layoutB, num_cu, a.ws_bytes);
+  return hip_status(mcg::launch_scaled(layoutB, a, num_cu, (hipStream_t)stream));
 }
 
 int mcg_validate_grad_i8(int dtypeA, int layoutA, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
@@ -299,9 +301,11 @@ int gemm_grad_i8(int dtypeA, int layoutA, int64_t M, int64_t N, int64_t K, const
   if (st != MCG_SUCCESS) return st;
   mcg::GradArgs a = grad_args(M, N, K, A, lda, Q, ldq, C, D, ldd, dtypeD, beta);
   a.sk = scaleK;
-  a.ws = (float*)workspace;
-  mcg::plan_grad(dtypeA, layoutA, a, current_num_cu(), workspace ? workspace_bytes : 0);
-  return hip_status(mcg::launch_grad(dtypeA, layoutA, a, (hipStream_t)stream));
+  a.ws = workspace;
+  a.ws_bytes = workspace ? workspace_bytes : 0;
+  const int num_cu = current_num_cu();
+  mcg::plan_grad(dtypeA, layoutA, a, num_cu, a.ws_bytes);
+  return hip_status(mcg::launch_grad(dtypeA, layoutA, a, num_cu, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -56,6 +56,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void* base, ui
   return __builtin_amdgcn_make_buffer_rsrc((void*)(((uint64_t)hi << 32) | lo), (short)0, (int)n, 0x00020000);
 }
 
+// Bytes from row 0, element x0 of an MN-contiguous operand (K rows of `width`
+// elements, ld apart) to its end, whole 16-byte chunks.
+__device__ __forceinline__ uint32_t mn_window(int64_t K, int64_t ld, int64_t width, int64_t x0, int eb) {
+  return (uint32_t)(((((K - 1) * ld + width) * eb + 15) & ~(int64_t)15) - x0 * eb);
+}
+
 // HBM -> LDS loader of one operand tile: wave w, instruction i of a stage
 // writes LDS bytes [(i * NW + w) * 1024, +1024) of that stage's tile.  K is
 // counted in elements of this operand.

@@ -40,7 +40,8 @@
 //     instructions and a K tile 2 barriers; 4 stages of A and of B (16 KiB each)
 //     with a prefetch distance of 3 tiles; at the end each wave hands its partner
 //     the 32-row block the partner stores, through LDS.  128 KiB of LDS: one
-//     workgroup per CU.  The host takes it for problems with too few 256 x 256
+//     workgroup per CU.  (64 x 128: the same with 32 x 64 quadrants, for the products
+//     of the 8-bit linear layer; gemm_fast_half.hip.)  The host takes it for problems with too few 256 x 256
 //     tiles when its cost model puts it ahead of the general kernel.
 // Preconditions (checked on the host): 16-byte aligned operands, K * elem_bytes
 // and ld * elem_bytes multiples of 16, M, N >= the tile size, and each workgroup's
@@ -49,9 +50,29 @@
 #include "fast_tiles.hpp"
 #include "frag_layout.hpp"
 #include "gemm_kernels.hpp"
+#include "scaled_epilogue.hpp"
 
 namespace mcg {
 namespace fast {
+
+// The int8 product with a scale per row and column (gemm_i8_scaled): the exact int32
+// sums of I8, another argument block and another epilogue.
+struct I8Scaled : I8 {};
+template <class Op>
+struct KernelTypes {
+  static constexpr bool SCALED = false;
+  using Args = DenseArgs;
+  using Dst = EpiDst;
+};
+struct ScaledDst : EpiDst {
+  const float *sa, *sb, *bias;  // sa null: raw int32 sums (a stream-K slot)
+};
+template <>
+struct KernelTypes<I8Scaled> {
+  static constexpr bool SCALED = true;
+  using Args = ScaledArgs;
+  using Dst = ScaledDst;
+};
 
 constexpr int KTB = 128;     // bytes of K per LDS row and stage: one 128-byte line per row
 constexpr int NSA = 2;       // LDS stages of A
@@ -62,12 +83,15 @@ constexpr int THREADS = 512;
 // fill the chip); each wavefront owns (TB / 2) x (TB / 4) outputs.  SK: the
 // stream-K form, whose workgroups each take a range of the K
 // iterations of the tiles after the first dp_tiles, which a launch of the
-// whole-tile form covers.
-template <class Op, int LA, int LB, int TB, bool SK = false>
+// whole-tile form covers.  TBM: rows of the output tile, TB, or 64 with TB = 128 for
+// problems with fewer 128 x 128 tiles than compute units.
+template <class Op, int LA, int LB, int TB, bool SK = false, int TBM = TB>
 __global__ __launch_bounds__(THREADS) __attribute__((amdgpu_waves_per_eu(2, 2)))
-void gemm_fast_kernel(DenseArgs p) {
-  constexpr int BM = TB, BN = TB;
-  constexpr int SB = TB * KTB;          // bytes of one operand stage
+void gemm_fast_kernel(typename KernelTypes<Op>::Args p) {
+  constexpr bool SCALED = KernelTypes<Op>::SCALED;
+  using Dst = typename KernelTypes<Op>::Dst;
+  constexpr int BM = TBM, BN = TB;
+  constexpr int SBA = BM * KTB, SB = BN * KTB;  // bytes of one stage of A and of B
   constexpr int EB = Op::EB;
   constexpr int LB16 = Op::LANE_BYTES;  // bytes of K per lane and instruction (16 or 32)
   constexpr int S = 64 / (2 * LB16);    // instructions per block and half K tile
@@ -75,7 +99,7 @@ void gemm_fast_kernel(DenseArgs p) {
   // and split every K tile, each multiplying one half; otherwise each covers half of
   // the quadrant's columns over all of K
   constexpr bool KS = TB == 128;
-  constexpr int WTM = TB / 64, WTN = KS ? 2 : TB / 128;  // 32 x 32 instruction tiles per wave
+  constexpr int WTM = BM / 64, WTN = KS ? 2 : TB / 128;  // 32 x 32 instruction tiles per wave
   // KS: prefetch distance KPD for both operands (KPD + 1 stages each, 128 KiB of LDS;
   // measured 3-15% faster than distance 2 over 1024..3072-row outputs, distance 4 slower)
   constexpr int KPD = 3;
@@ -91,26 +115,27 @@ void gemm_fast_kernel(DenseArgs p) {
   using frag_t = typename Op::frag_t;
   using v4 = typename std::conditional<Op::INT_ACC, i32x4, f32x4>::type;
   using s1 = typename std::conditional<Op::INT_ACC, int, float>::type;
-  static_assert(TB == 256 || TB == 128, "tile");
-  static_assert(GA::BYTES == SB && GB::BYTES == SB, "one stage size for both operands");
-  constexpr int LH = LdA::INSTR / 2;  // loads per wave, operand and half stage (one group's share)
-  static_assert(LdA::INSTR == LdB::INSTR && (LH == 4 || LH == 2), "vmcnt bookkeeping");
+  static_assert((TB == 256 && BM == 256) || (TB == 128 && (BM == 128 || (BM == 64 && !SK))), "tile");
+  static_assert(GA::BYTES == SBA && GB::BYTES == SB, "stage sizes");
+  // loads per wave and half stage (one group's share) of A and of B
+  constexpr int LHA = LdA::INSTR / 2, LH = LdB::INSTR / 2;
+  static_assert(LH == 4 || LH == 2, "vmcnt bookkeeping");
 
-  __shared__ __attribute__((aligned(1024))) char smem_raw[(NA + NB) * SB];
+  __shared__ __attribute__((aligned(1024))) char smem_raw[NA * SBA + NB * SB];
   lds_char* smem = (lds_char*)smem_raw;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int grp = wave >> 2;  // 0: multiplies in even slots; 1: in odd slots
   const int q = wave & 3;     // wavefronts q and q + 4 share a SIMD and a quadrant of the tile
-  const int rbA = (q >> 1) * (TB / 2), rbB = (q & 1) * (TB / 2) + (KS ? 0 : grp * (TB / 4));
+  const int rbA = (q >> 1) * (BM / 2), rbB = (q & 1) * (TB / 2) + (KS ? 0 : grp * (TB / 4));
   const int g = lane >> 5;
 
   const int nk_all = (int)((p.K + KTB / EB - 1) / (KTB / EB));  // K tiles of the problem
 
   // One piece of work: K tiles [kb, kb + nk) of output tile (tm, tn), whose
   // epilogue writes to d.
-  auto work = [&](int tm, int tn, int kb, int nk, const EpiDst& d) {
+  auto work = [&](int tm, int tn, int kb, int nk, const Dst& d) {
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
 
   LdA la;
@@ -118,11 +143,11 @@ void gemm_fast_kernel(DenseArgs p) {
   if constexpr (LA == LAYOUT_K)
     la.init(p.A + m0 * p.lda * EB, (uint32_t)(min(p.M - m0, (int64_t)BM) * p.lda * EB), p.lda, p.K, q, lane);
   else
-    la.init(p.A + m0 * EB, (uint32_t)((p.K * p.lda - m0) * EB), p.lda, p.K, q, lane);
+    la.init(p.A + m0 * EB, mn_window(p.K, p.lda, p.M, m0, EB), p.lda, p.K, q, lane);
   if constexpr (LB == LAYOUT_K)
     lb.init(p.B + n0 * p.ldb * EB, (uint32_t)(min(p.N - n0, (int64_t)BN) * p.ldb * EB), p.ldb, p.K, q, lane);
   else
-    lb.init(p.B + n0 * EB, (uint32_t)((p.K * p.ldb - n0) * EB), p.ldb, p.K, q, lane);
+    lb.init(p.B + n0 * EB, mn_window(p.K, p.ldb, p.N, n0, EB), p.ldb, p.K, q, lane);
 
   acc_t acc[WTM][WTN];
 #pragma unroll
@@ -130,12 +155,11 @@ void gemm_fast_kernel(DenseArgs p) {
 #pragma unroll
     for (int j = 0; j < WTN; ++j) acc[i][j] = acc_t{};
 
-  auto stA = [&](int kt) { return smem + (KS ? kt % NA : kt & 1) * SB; };
-  auto stB = [&](int kt) { return smem + NA * SB + (kt % NB) * SB; };
+  auto stA = [&](int kt) { return smem + (KS ? kt % NA : kt & 1) * SBA; };
+  auto stB = [&](int kt) { return smem + NA * SBA + (kt % NB) * SB; };
   // this group's half (LH of the 2 LH load instructions per wave) of operand X of K tile kt
-  const int ihalf = LH * grp;
-  auto issueA = [&](int kt) { la.issue(stA(kt), kb + kt, ihalf, LH, q); };
-  auto issueB = [&](int kt) { lb.issue(stB(kt), kb + kt, ihalf, LH, q); };
+  auto issueA = [&](int kt) { la.issue(stA(kt), kb + kt, LHA * grp, LHA, q); };
+  auto issueB = [&](int kt) { lb.issue(stB(kt), kb + kt, LH * grp, LH, q); };
 
   frag_t fa[S][WTM], fb[S][WTN];
   // fragments of half h (K bytes [64h, 64h + 64) of each row) of K tile kt;
@@ -145,10 +169,10 @@ void gemm_fast_kernel(DenseArgs p) {
   // ordinary reads.  A lane's 4 transposing reads of a 32-row block lie TR_O1,
   // TR_O2, TR_O3 bytes after the first: the second read of a 16-byte part is 4
   // (16-bit) or 8 (8-bit) rows further, the next part 16 or 32 rows.
-  constexpr int TRW = TB * EB;  // bytes per LDS row (one k) of an MN-contiguous tile
-  constexpr int TR_O1 = EB == 2 ? 4 * TRW : 8 * TRW;
-  constexpr int TR_O2 = (LB16 == 32 || EB == 2) ? 16 * TRW : 32 * TRW;
-  constexpr int TR_O3 = TR_O2 + TR_O1;
+  constexpr int TRW = TB * EB, TRWA = BM * EB;  // bytes per LDS row (one k) of an MN-contiguous tile
+  constexpr int TR_R1 = EB == 2 ? 4 : 8, TR_R2 = (LB16 == 32 || EB == 2) ? 16 : 32;  // rows
+  constexpr int TR_O1 = TR_R1 * TRW, TR_O2 = TR_R2 * TRW, TR_O3 = TR_O2 + TR_O1;
+  constexpr int TR_A1 = TR_R1 * TRWA, TR_A2 = TR_R2 * TRWA, TR_A3 = TR_A2 + TR_A1;
   constexpr int NTA = LA == LAYOUT_MN ? WTM : 0, NTB = LB == LAYOUT_MN ? WTN : 0;
   auto unpack = [&](const i32x2 (&r)[4], frag_t& f0, frag_t& f1) {
     if constexpr (LB16 == 16) {
@@ -197,7 +221,23 @@ void gemm_fast_kernel(DenseArgs p) {
       if constexpr (NTB > 0)
 #pragma unroll
         for (int j = 0; j < NTB; ++j) ad[NTA + j] = RB::mn_addr(stB(kt), rbB + 32 * j, kb0, lane);
-      lds_read_tr_x4<EB, TR_O1, TR_O2, TR_O3>(ad, r);
+      if constexpr (NTA > 0 && NTB > 0 && TRWA != TRW) {  // rows of two lengths: a block each
+        static_assert(NTA == 1 && NTB == 2, "64 x 128 tile");
+        const uint32_t ada[1] = {ad[0]}, adb[2] = {ad[1], ad[2]};
+        i32x2 ra[1][4], rb[2][4];
+        lds_read_tr_x4<EB, TR_A1, TR_A2, TR_A3>(ada, ra);
+        lds_read_tr_x4<EB, TR_O1, TR_O2, TR_O3>(adb, rb);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          r[0][u] = ra[0][u];
+          r[1][u] = rb[0][u];
+          r[2][u] = rb[1][u];
+        }
+      } else if constexpr (NTA > 0) {
+        lds_read_tr_x4<EB, TR_A1, TR_A2, TR_A3>(ad, r);
+      } else {
+        lds_read_tr_x4<EB, TR_O1, TR_O2, TR_O3>(ad, r);
+      }
 #pragma unroll
       for (int i = 0; i < NTA; ++i) unpack(r[i], fa[0][i], fa[S - 1][i]);
 #pragma unroll
@@ -242,14 +282,14 @@ void gemm_fast_kernel(DenseArgs p) {
     // next slot.  Each memory phase issues this wave's shares of A(t+KPD) and
     // B(t+KPD) into the stages of tile t-1 (stage index mod KPD + 1; last read in
     // slot 2t - 2); at the end of slot 2t each wave waits until only the loads of
-    // tiles t+2 .. t+KPD ((KPD - 1) 2 LH) are in flight, so tile t+1 is complete
+    // tiles t+2 .. t+KPD ((KPD - 1) (LHA + LH)) are in flight, so tile t+1 is complete
     // from slot 2t + 1.
 #pragma unroll
     for (int t0 = 0; t0 < KPD; ++t0) {
       issueA(t0);
       issueB(t0);
     }
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((KPD - 1) * 2 * LH) : "memory");  // own shares of tile 0
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((KPD - 1) * (LHA + LH)) : "memory");  // own shares of tile 0
     barrier_lds();
     if (grp == 0) {
       for (int t = 0; t < nk; ++t) {
@@ -261,7 +301,7 @@ void gemm_fast_kernel(DenseArgs p) {
         __builtin_amdgcn_sched_barrier(0);
         multiply();  // slot 2t
         __builtin_amdgcn_sched_barrier(0);
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((KPD - 1) * 2 * LH) : "memory");  // own shares of tile t+1
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((KPD - 1) * (LHA + LH)) : "memory");  // own shares of tile t+1
         barrier_lds();
       }
     } else {
@@ -271,7 +311,7 @@ void gemm_fast_kernel(DenseArgs p) {
         issueA(t + KPD);
         issueB(t + KPD);
         read_frags(t, 1);  // slot 2t
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((KPD - 1) * 2 * LH) : "memory");  // own shares of tile t+1
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((KPD - 1) * (LHA + LH)) : "memory");  // own shares of tile t+1
         barrier_lds();
         __builtin_amdgcn_sched_barrier(0);
         multiply();  // slot 2t + 1
@@ -329,7 +369,8 @@ void gemm_fast_kernel(DenseArgs p) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no LDS DMA outstanding at exit
   if constexpr (KS) {
     // Sum the two K halves: wave w hands its partner (w ^ 4) the 32-row block
-    // i = 1 - grp, which the partner stores, through 8 KiB of LDS per wave.
+    // i = 1 - grp, which the partner stores, through 8 KiB of LDS per wave.  (64-row
+    // tiles have one block per pair: group 1 hands it over and stores nothing.)
     using e1 = typename std::conditional<Op::INT_ACC, int, float>::type;
     typedef __attribute__((address_space(3))) e1 lds_e1;
     barrier_lds();  // all LDS DMA has landed; no fragment reads remain
@@ -352,11 +393,17 @@ void gemm_fast_kernel(DenseArgs p) {
             blk[j][r] += theirs[(j * 16 + r) * 64 + lane];
         }
     };
-    if (grp == 0) put(acc[1]);
-    else put(acc[0]);
-    barrier_lds();
-    if (grp == 0) add(acc[0]);
-    else add(acc[1]);
+    if constexpr (WTM == 1) {
+      if (grp == 1) put(acc[0]);
+      barrier_lds();
+      if (grp == 0) add(acc[0]);
+    } else {
+      if (grp == 0) put(acc[1]);
+      else put(acc[0]);
+      barrier_lds();
+      if (grp == 0) add(acc[0]);
+      else add(acc[1]);
+    }
   }
 
   // epilogue: each instruction multiplied (B fragment) x (A fragment), so element
@@ -372,7 +419,7 @@ void gemm_fast_kernel(DenseArgs p) {
   const bool vec_ok = d.vec;
   const s1* C = (const s1*)d.C;
   s1* D = (s1*)d.D;
-  if constexpr (Op::INT_ACC) {
+  if constexpr (Op::INT_ACC && !SCALED) {
     // wrapping alpha * acc, in place (keeps the products out of the C batches)
     if (d.alpha_i != 1) {
 #pragma unroll
@@ -422,6 +469,57 @@ void gemm_fast_kernel(DenseArgs p) {
       }
       return o;
     };
+    // Row group i from the accumulator layout to 8 x (4 columns of row 4t + rr) per
+    // lane; between(): issued once the accumulators are staged.
+    auto through_lds = [&](int i, lds_char* buf, v4 (&a)[8], auto between) {
+#pragma unroll
+      for (int j = 0; j < WTN; ++j)
+#pragma unroll
+        for (int r4 = 0; r4 < 4; ++r4) {
+          const int ch = (32 * j + acc_n(r4)) / 4;  // 16-byte chunk of the wavefront's 64 columns
+          v4 x;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) x[r] = acc[i][j][4 * r4 + r];
+          *(lds_v4*)(buf + wr * 256 + ((ch ^ (wr & 15)) << 4)) = x;
+        }
+      between();
+      // the reads below take other lanes' values: wait for the writes
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const int row = 4 * t + rr;
+        a[t] = *(const lds_v4*)(buf + row * 256 + ((cc ^ (row & 15)) << 4));
+      }
+    };
+    if constexpr (SCALED) {
+      if (d.sa) {
+        float sb[4], bias[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sb[e] = d.sb[col + e];
+          bias[e] = d.bias ? d.bias[col + e] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < WTM; ++i) {
+          __builtin_amdgcn_sched_barrier(0);
+          if (KS && i != grp) continue;  // the partner wave stores this row block
+          const int64_t row0 = em0 + rbA + 32 * i + rr;
+          float sa[8];
+#pragma unroll
+          for (int t = 0; t < 8; ++t) sa[t] = d.sa[row0 + 4 * t];
+          v4 a[8];
+          through_lds(i, wbuf + (KS ? 0 : (i & 1) * 8192), a, [] {});
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            float o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = scaled_value(a[t][e], sa[t], sb[e], bias[e]);
+            scaled_put4(d.D, (row0 + 4 * t) * d.ld + col, out, o, true, 4);
+          }
+        }
+        return;
+      }
+    }
     // The passes over the row blocks, for binary32 / int32 (O16 false) or 16-bit
     // (O16 true) C and D.  Each pass's C rows are loaded one pass ahead: pass i + 1's
     // loads go out once pass i has staged its accumulators (whose registers they
@@ -443,7 +541,7 @@ void gemm_fast_kernel(DenseArgs p) {
             cn[t] = __builtin_nontemporal_load((const v4*)(C + rb + 4 * t * d.ld));
         }
       };
-      if (d.use_c) load_c(KS ? grp : 0);
+      if (d.use_c) load_c(KS && WTM > 1 ? grp : 0);
 #pragma unroll
       for (int i = 0; i < WTM; ++i) {
         __builtin_amdgcn_sched_barrier(0);
@@ -453,25 +551,10 @@ void gemm_fast_kernel(DenseArgs p) {
         cvec cv[8];
 #pragma unroll
         for (int t = 0; t < 8; ++t) cv[t] = cn[t];
-#pragma unroll
-        for (int j = 0; j < WTN; ++j)
-#pragma unroll
-          for (int r4 = 0; r4 < 4; ++r4) {
-            const int ch = (32 * j + acc_n(r4)) / 4;  // 16-byte chunk of the wavefront's 64 columns
-            v4 x;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x[r] = acc[i][j][4 * r4 + r];
-            *(lds_v4*)(buf + wr * 256 + ((ch ^ (wr & 15)) << 4)) = x;
-          }
-        if (!KS && i + 1 < WTM && d.use_c) load_c(i + 1);
-        // the reads below take other lanes' values: wait for the writes
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         v4 a[8];
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          const int row = 4 * t + rr;
-          a[t] = *(const lds_v4*)(buf + row * 256 + ((cc ^ (row & 15)) << 4));
-        }
+        through_lds(i, buf, a, [&] {
+          if (!KS && i + 1 < WTM && d.use_c) load_c(i + 1);
+        });
         if constexpr (O16) {
           uint16_t* D16 = (uint16_t*)d.D;
 #pragma unroll
@@ -551,6 +634,30 @@ void gemm_fast_kernel(DenseArgs p) {
       return;
     }
   }
+  if constexpr (SCALED) {
+    if (d.sa) {
+#pragma unroll
+      for (int i = 0; i < WTM; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (KS && i != grp) continue;  // the partner wave stores this row block
+        const int64_t m = em0 + rbA + 32 * i + acc_m;
+        if (m >= d.M) continue;
+        const float sa = d.sa[m];
+#pragma unroll
+        for (int j = 0; j < WTN; ++j)
+#pragma unroll
+          for (int r4 = 0; r4 < 4; ++r4) {
+            const int64_t n = en0 + rbB + 32 * j + acc_n(r4);
+            if (n >= d.N) continue;
+            i32x4 v;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = acc[i][j][4 * r4 + r];
+            scaled_store4(p, m, n, v, sa);
+          }
+      }
+      return;
+    }
+  }
   {
     // edge tile: per-element bounds
 #pragma unroll
@@ -584,14 +691,19 @@ void gemm_fast_kernel(DenseArgs p) {
   }
   };  // work
 
+  // the destination of a whole tile
+  auto whole_tile = [&](int tm, int tn) {
+    const EpiDst e{p.D, p.C, p.ldc, p.M, p.N, (int64_t)tm * BM, (int64_t)tn * BN, p.alpha, p.beta, p.alpha_i,
+                   p.beta_i, p.use_c, p.vec_cd, p.out};
+    if constexpr (SCALED) return Dst{e, p.sa, p.sb, p.bias};
+    else return e;
+  };
   if constexpr (!SK) {
     // XCD-aware, grouped tile order over all tiles, or over the first dp_tiles
     // tiles when the rest are left to the stream-K form
     int tm, tn;
     tile_coords_of<4>(blockIdx.x, p.dp_tiles > 0 ? p.dp_tiles : p.tiles_m * p.tiles_n, p.tiles_m, p.tiles_n, tm, tn);
-    work(tm, tn, 0, nk_all,
-         EpiDst{p.D, p.C, p.ldc, p.M, p.N, (int64_t)tm * BM, (int64_t)tn * BN, p.alpha, p.beta, p.alpha_i,
-                p.beta_i, p.use_c, p.vec_cd, p.out});
+    work(tm, tn, 0, nk_all, whole_tile(tm, tn));
   } else {
     // Workgroup w takes K iterations [w L, (w + 1) L) of the tiles after the
     // first dp_tiles (which a whole-tile launch covers), numbered tile by tile:
@@ -615,10 +727,13 @@ void gemm_fast_kernel(DenseArgs p) {
       }
       if (pc > 0) barrier_lds();  // the previous piece's epilogue is done with the LDS
       const bool whole = kbeg == 0 && kcnt == nk_all;
-      const EpiDst d = whole ? EpiDst{p.D, p.C, p.ldc, p.M, p.N, (int64_t)tm * BM, (int64_t)tn * BN, p.alpha,
-                                      p.beta, p.alpha_i, p.beta_i, p.use_c, p.vec_cd, p.out}
-                             : EpiDst{(char*)p.ws + piece * (int64_t)(TB * TB * 4), nullptr, TB, TB, TB, 0, 0,
-                                      1.0f, 0.0f, 1, 0, 0, 1, OUT_32};
+      Dst d = whole_tile(tm, tn);
+      if (!whole) {
+        const EpiDst slot{(char*)p.ws + piece * (int64_t)(TB * TB * 4), nullptr, TB, TB, TB, 0, 0,
+                          1.0f, 0.0f, 1, 0, 0, 1, OUT_32};
+        if constexpr (SCALED) d = Dst{slot, nullptr, nullptr, nullptr};
+        else d = slot;
+      }
       work(tm, tn, kbeg, kcnt, d);
       it += kcnt;
       ++piece;
@@ -634,8 +749,8 @@ void gemm_fast_kernel(DenseArgs p) {
 // row; up to FIX_BATCH pieces are loaded before they are added, so that the
 // loads overlap.
 constexpr int FIX_BATCH = 8;
-template <bool INT, int TB>
-__global__ __launch_bounds__(256) void streamk_fixup_kernel(DenseArgs p, int64_t nk) {
+template <bool INT, int TB, class Args = DenseArgs>
+__global__ __launch_bounds__(256) void streamk_fixup_kernel(Args p, int64_t nk) {
   const int64_t x = blockIdx.x, L = p.sk_iters;
   const int64_t w0 = x * nk / L, w1 = ((x + 1) * nk - 1) / L;  // workgroups with a piece of tile x
   if (w0 == w1) return;  // one piece: the whole tile, stored by its workgroup
@@ -667,6 +782,10 @@ __global__ __launch_bounds__(256) void streamk_fixup_kernel(DenseArgs p, int64_t
         }
       }
   }
+  if constexpr (std::is_same<Args, ScaledArgs>::value) {
+    scaled_store4(p, m, n, acc, p.sa[m]);
+    return;
+  } else {
   const int64_t doff = m * p.ldc + n;
   const bool full = p.vec_cd && n + 4 <= p.N;
   e1 o[4];
@@ -704,18 +823,20 @@ __global__ __launch_bounds__(256) void streamk_fixup_kernel(DenseArgs p, int64_t
       D16[doff + e] = (uint16_t)to_out_bits(p.out, v);
     }
   }
+  }
 }
 
-template <class Op, int LA, int LB, int TB, bool SK = false>
-hipError_t launch_one(const DenseArgs& a0, hipStream_t s) {
-  DenseArgs a = a0;
-  a.tiles_m = (int)((a.M + TB - 1) / TB);
+template <class Op, int LA, int LB, int TB, bool SK = false, int TBM = TB>
+hipError_t launch_one(const typename KernelTypes<Op>::Args& a0, hipStream_t s) {
+  using Args = typename KernelTypes<Op>::Args;
+  Args a = a0;
+  a.tiles_m = (int)((a.M + TBM - 1) / TBM);
   a.tiles_n = (int)((a.N + TB - 1) / TB);
   const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
   if (tiles <= 0) return hipSuccess;
   hipError_t e = hipSuccess;
   if (!SK || a.dp_tiles > 0) {  // whole tiles: every tile, or the first dp_tiles
-    hipLaunchKernelGGL((gemm_fast_kernel<Op, LA, LB, TB, false>), dim3((unsigned)(SK ? a.dp_tiles : tiles)),
+    hipLaunchKernelGGL((gemm_fast_kernel<Op, LA, LB, TB, false, TBM>), dim3((unsigned)(SK ? a.dp_tiles : tiles)),
                        dim3(THREADS), 0, s, a);
     e = hipGetLastError();
   }
@@ -725,7 +846,7 @@ hipError_t launch_one(const DenseArgs& a0, hipStream_t s) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t nk = (a.K + KTB / Op::EB - 1) / (KTB / Op::EB);
-    hipLaunchKernelGGL((streamk_fixup_kernel<Op::INT_ACC, TB>), dim3((unsigned)a.sk_tiles, TB * TB / 1024), dim3(256), 0, s,
+    hipLaunchKernelGGL((streamk_fixup_kernel<Op::INT_ACC, TB, Args>), dim3((unsigned)a.sk_tiles, TB * TB / 1024), dim3(256), 0, s,
                        a, nk);
     e = hipGetLastError();
   }

@@ -21,6 +21,8 @@
 // General kernel: 128 x 128 tiles, 4 wavefronts, any size, pointer and leading
 // dimension.  Q's tile is widened on its way from the registers to LDS, where it is
 // an ordinary 16-bit MN-contiguous tile.
+#include <algorithm>
+
 #include "linear8.hpp"
 #include "row_vec.hpp"
 #include "tile_any.hpp"
@@ -110,7 +112,7 @@ __global__ __launch_bounds__(256) void grad_general_kernel(GradArgs p) {
     for (int t = 0; t < QPT; ++t) {
       const int c = tid + t * NT;
       const int64_t k = k0 + c / QCPR, n = n0 + 16 * (c % QCPR);
-      q[t] = load_chunk<1>(p.Q + k * p.ldq + n, k < p.K ? p.N - n : 0);
+      q[t] = load_chunk(p.Q, p.Q + k * p.ldq + n, k < p.K ? p.N - n : 0);
       s[t] = k < p.K ? p.sk[k] : 0.0f;
     }
   };
@@ -173,7 +175,7 @@ __global__ __launch_bounds__(256) void grad_general_kernel(GradArgs p) {
       const int64_t n = n0 + wn * 64 + j * 16 + acc_n;
       if (n >= p.N) continue;
       if (p.splits > 1) {
-        float* w = p.ws + ((int64_t)blockIdx.y * p.M + m) * p.N + n;
+        float* w = (float*)p.ws + ((int64_t)blockIdx.y * p.M + m) * p.N + n;
         for (int e = 0; e < 4; ++e)
           if (n + e < p.N) w[e] = acc[i][j][e];
       } else {
@@ -190,7 +192,7 @@ __global__ __launch_bounds__(256) void grad_finish_kernel(GradArgs p) {
   for (int64_t m = blockIdx.y; m < p.M; m += gridDim.y) {
     f32x4 acc = {0, 0, 0, 0};
     for (int s = 0; s < p.splits; ++s) {
-      const float* w = p.ws + ((int64_t)s * p.M + m) * p.N + n;
+      const float* w = (const float*)p.ws + ((int64_t)s * p.M + m) * p.N + n;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (n + e < p.N) acc[e] += w[e];
@@ -199,17 +201,150 @@ __global__ __launch_bounds__(256) void grad_finish_kernel(GradArgs p) {
   }
 }
 
-int64_t plan_grad(int, int, GradArgs& a, int num_cu, int64_t ws_bytes) {
-  const int64_t nk = (a.K + KT_BYTES / 2 - 1) / (KT_BYTES / 2);
-  a.tiles_m = (int)((a.M + 127) / 128);
-  a.tiles_n = (int)((a.N + 127) / 128);
+// A panel: columns [n0, n0 + nc) of s[k] Q[k][j] in A's type, ldw apart, zeros past nc
+// and past row K; with TWO a second panel of the rests at lo.  16 codes per thread.
+template <class Op, bool TWO>
+__global__ __launch_bounds__(256) void grad_widen_kernel(const char* Q, const float* sk, int64_t K, int64_t ldq, int64_t n0,
+                                                         int64_t nc, char* hi, char* lo, int64_t ldw, uint32_t cpr,
+                                                         uint32_t chunks) {
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= chunks) return;
+  const int64_t k = i / cpr, c = 16 * (int64_t)(i % cpr);
+  const float s = k < K ? sk[k] : 0.0f;
+  i32x4 h[2], l[2];
+  widen16<Op, TWO>(load_chunk(Q, Q + k * ldq + n0 + c, k < K ? nc - c : 0), s, h, l);
+  char* d = hi + (k * ldw + c) * 2;
+  *(i32x4*)d = h[0];
+  *(i32x4*)(d + 16) = h[1];
+  if constexpr (TWO) {
+    d = lo + (k * ldw + c) * 2;
+    *(i32x4*)d = l[0];
+    *(i32x4*)(d + 16) = l[1];
+  }
+}
+
+namespace {
+int64_t cdiv(int64_t x, int64_t y) { return (x + y - 1) / y; }
+int64_t round_up(int64_t x, int64_t y) { return cdiv(x, y) * y; }
+constexpr int64_t PANEL_STEP = 256;  // columns of a panel come in whole tiles
+
+// Bytes of the copy of A and of the panels, at the workspace's start.
+int64_t copy_bytes(int la, const GradArgs& a) { return a.lda2 ? a.lda2 * 2 * (la == LAYOUT_K ? a.M : a.K) : 0; }
+int64_t panel_bytes(const GradArgs& a) { return a.ka * a.ldw * 2; }
+
+// The dense product of A (or its copy) with a panel of nc columns.
+DenseArgs dense_args(int la, const GradArgs& a, int64_t nc) {
+  DenseArgs d{};
+  d.A = a.lda2 ? (const char*)a.ws : a.A;
+  d.lda = a.lda2 ? a.lda2 : a.lda;
+  d.ldb = a.ldw;
+  d.M = a.M;
+  d.N = nc;
+  d.K = a.ka;
+  d.ldc = a.ldd;
+  d.alpha = 1.0f;
+  d.beta = a.beta;
+  d.use_c = a.use_c;
+  d.out = a.out;
+  d.vec_cd = a.vec_d;
+  return d;
+}
+
+// Fills the panel fields for ws_bytes of workspace: the modelled time and the bytes
+// used, or a negative time when the operands' offsets or the workspace rule it out.
+double plan_panels(int dtA, int la, GradArgs& a, int num_cu, int64_t ws_bytes, int64_t* used) {
+  const int64_t two = a.out == OUT_32 ? 2 : 1;
+  const bool chunks = (uintptr_t)a.A % 16 == 0 && a.lda % 8 == 0 && (la == LAYOUT_MN || a.K % 8 == 0);
+  a.ka = chunks || la == LAYOUT_MN ? a.K : round_up(a.K, 8);
+  a.lda2 = chunks ? 0 : round_up(la == LAYOUT_K ? a.K : a.M, 8);
+  const int64_t fixed = copy_bytes(la, a), lim = (int64_t)1 << 31;
+  const int64_t lda = a.lda2 ? a.lda2 : a.lda;
+  if ((la == LAYOUT_K ? 256 * lda : (a.ka + 256) * lda) * 2 >= lim || fixed / 16 >= lim || fixed >= ws_bytes) return -1.0;
+  // the widest panel that fits, cut into equal ones
+  const int64_t fit = (ws_bytes - fixed) / (a.ka * 2 * two);
+  const int64_t most = std::min((lim - 1) / ((a.ka + 256) * 2), fit) / 16 * 16;  // (a panel's offsets below 2 GiB)
+  if (most < round_up(a.N, 16) && most < PANEL_STEP) return -1.0;
+  const int64_t count = most >= round_up(a.N, 16) ? 1 : cdiv(a.N, most / PANEL_STEP * PANEL_STEP);
+  a.panel_n = count == 1 ? a.N : round_up(cdiv(a.N, count), PANEL_STEP);
+  a.ldw = round_up(a.panel_n, 16);
+  const int64_t panels = fixed + two * panel_bytes(a);
+  DenseArgs d = dense_args(la, a, a.panel_n);
+  const PipePlan pp = plan_pipe(dtA, d, num_cu, ws_bytes - panels);
+  *used = panels + pp.ws;
+  const double widen = pass_us((double)a.ka * a.ldw * (1 + 2 * two));
+  return (fixed > 0 ? pass_us(2.0 * fixed) : 0.0) + cdiv(a.N, a.panel_n) * (widen + two * pp.us);
+}
+}  // namespace
+
+// Two ways: the general kernel widens Q's tiles on their way to LDS, once for every
+// 128 rows of A, and takes any operands; panels widen Q once into the workspace (a
+// copy's time for 3 or 5 bytes an element) and multiply on the pipelined dense
+// kernels, at about half the time per product.  The modelled times decide: PANEL_NOTE
+int64_t plan_grad(int dtA, int la, GradArgs& a, int num_cu, int64_t ws_bytes) {
+  const int64_t nk = cdiv(a.K, KT_BYTES / 2);
+  a.tiles_m = (int)cdiv(a.M, 128);
+  a.tiles_n = (int)cdiv(a.N, 128);
   const int64_t slot = a.M * a.N * 4;
   const int64_t most = slot > 0 ? ws_bytes / slot : 1;
-  const int64_t s = plan_ranges((int64_t)a.tiles_m * a.tiles_n, nk, a.M * a.N, num_cu, a.out == OUT_32 ? 1.5 : 1.0,
-                                most < 64 ? most : 64);
-  a.kt_per_split = (int)(nk > 0 ? (nk + s - 1) / s : 1);
+  double general_us;
+  const int64_t s = plan_ranges((int64_t)a.tiles_m * a.tiles_n, nk, a.M * a.N, num_cu, a.out == OUT_32 ? 1.5 : 0.9,
+                                most < 64 ? most : 64, &general_us);
+  a.kt_per_split = (int)(nk > 0 ? cdiv(nk, s) : 1);
   a.splits = (int)s;
+  if (a.K > 0) {
+    int64_t used = 0;
+    const double us = plan_panels(dtA, la, a, num_cu, ws_bytes, &used);
+    if (us > 0.0 && us < general_us) return used;
+  }
+  a.panel_n = 0;
   return s > 1 ? s * slot : 0;
+}
+
+template <class Op>
+static hipError_t launch_widen(const GradArgs& a, int64_t n0, int64_t nc, char* hi, char* lo, hipStream_t s) {
+  const int64_t cpr = a.ldw / 16, chunks = cpr * a.ka;
+  const dim3 grid((unsigned)cdiv(chunks, 256));
+  if (lo)
+    hipLaunchKernelGGL((grad_widen_kernel<Op, true>), grid, dim3(256), 0, s, a.Q, a.sk, a.K, a.ldq, n0, nc, hi, lo, a.ldw,
+                       (uint32_t)cpr, (uint32_t)chunks);
+  else
+    hipLaunchKernelGGL((grad_widen_kernel<Op, false>), grid, dim3(256), 0, s, a.Q, a.sk, a.K, a.ldq, n0, nc, hi, lo, a.ldw,
+                       (uint32_t)cpr, (uint32_t)chunks);
+  return hipGetLastError();
+}
+
+// Panels: binary32 results take the product with the rests first, then add the other.
+static hipError_t launch_panels(int dtA, int la, const GradArgs& a, int num_cu, hipStream_t s) {
+  const bool two = a.out == OUT_32;
+  const int64_t eo = two ? 4 : 2, fixed = copy_bytes(la, a);
+  char* hi = (char*)a.ws + fixed;
+  char* lo = two ? hi + panel_bytes(a) : nullptr;
+  char* slots = hi + (two ? 2 : 1) * panel_bytes(a);
+  hipError_t e = hipSuccess;
+  if (a.lda2)
+    e = la == LAYOUT_K ? launch_align_rows(a.A, a.lda * 2, a.M, a.K * 2, a.ws, a.lda2 * 2, a.M, s)
+                       : launch_align_rows(a.A, a.lda * 2, a.K, a.M * 2, a.ws, a.lda2 * 2, a.K, s);
+  for (int64_t n0 = 0; n0 < a.N && e == hipSuccess; n0 += a.panel_n) {
+    const int64_t nc = std::min(a.panel_n, a.N - n0);
+    e = dtA == DT_BF16 ? launch_widen<OpBF16>(a, n0, nc, hi, lo, s) : launch_widen<OpF16>(a, n0, nc, hi, lo, s);
+    for (int part = two ? 0 : 1; part < 2 && e == hipSuccess; ++part) {
+      DenseArgs d = dense_args(la, a, nc);
+      d.B = part == 0 ? lo : hi;
+      d.D = (char*)a.D + n0 * eo;
+      d.C = a.use_c ? (const char*)a.C + n0 * eo : nullptr;
+      if (two && part == 1) {
+        d.C = d.D;
+        d.beta = 1.0f;
+        d.use_c = 1;
+      }
+      d.ws = slots;
+      const PipePlan pp = plan_pipe(dtA, d, num_cu, a.ws_bytes - (slots - (char*)a.ws));
+      e = pp.tile == 64 ? launch_fast_half(dtA, la, d, s)
+          : pp.ws > 0   ? launch_fast_sk(dtA, dtA, la, LAYOUT_MN, d, s, pp.tile)
+                        : launch_fast(dtA, dtA, la, LAYOUT_MN, d, s, pp.tile);
+    }
+  }
+  return e;
 }
 
 template <class Op>
@@ -224,7 +359,8 @@ static void launch_general(int la, const GradArgs& a, dim3 grid, hipStream_t s) 
   }
 }
 
-hipError_t launch_grad(int dtA, int layoutA, const GradArgs& a, hipStream_t s) {
+hipError_t launch_grad(int dtA, int layoutA, const GradArgs& a, int num_cu, hipStream_t s) {
+  if (a.panel_n > 0) return launch_panels(dtA, layoutA, a, num_cu, s);
   const int64_t blocks = (int64_t)a.tiles_m * a.tiles_n;
   if (blocks > 0xffffff) return hipErrorInvalidValue;  // (a launch holds less than 2^32 threads)
   const dim3 grid((unsigned)blocks, (unsigned)a.splits);

@@ -30,6 +30,7 @@
 // (32-bit buffer offsets).
 #include "fast_tiles.hpp"
 #include "gemm_kernels.hpp"
+#include "scaled_epilogue.hpp"
 
 namespace mcg {
 namespace stream {
@@ -90,14 +91,34 @@ struct StreamFrag {
   }
 };
 
+// The int8 product with a scale per row and column: another argument block and epilogue.
+struct I8Scaled : I8 {};
+template <class Op>
+struct StreamArgs {
+  using type = DenseArgs;
+  template <int BW>
+  static constexpr int steps() { return 1; }
+};
+template <>
+struct StreamArgs<I8Scaled> {
+  using type = ScaledArgs;
+  // K tiles between two workgroup barriers.  A barrier, the fragments' LDS reads and
+  // their wait take about 450 cycles, which one tile of 32 rows (4 KiB of the wide
+  // operand) does not pay for: STEPS_NOTE
+  template <int BW>
+  static constexpr int steps() { return BW == 32 ? 3 : BW == 64 ? 2 : 1; }
+};
+
 template <class Op, int LA, int LB, bool WIDE_A, int BW>
-__global__ __launch_bounds__(THREADS) void gemm_stream_kernel(DenseArgs p) {
+__global__ __launch_bounds__(THREADS) void gemm_stream_kernel(typename StreamArgs<Op>::type p) {
   constexpr int EB = Op::EB;
   constexpr int LB16 = Op::LANE_BYTES;         // bytes of K per lane and instruction (16 or 32)
   constexpr int SPS = KTB / (2 * LB16);        // instructions per stage
   constexpr int RBLK = BW / 32;                // 32-row blocks of the wide operand
   constexpr int KG = NW / RBLK;                // wavefronts sharing one block, splitting K
-  constexpr int NS = ring_stages<EB, BW>();
+  constexpr int U = StreamArgs<Op>::template steps<BW>();  // K tiles per barrier
+  constexpr int NG = ring_stages<EB, BW>() / U;            // groups of U stages in the ring
+  constexpr int NS = NG * U;
   constexpr int RA_ROWS = WIDE_A ? BW : NR, RB_ROWS = WIDE_A ? NR : BW;
   using GA = Geom<EB, LA, RA_ROWS, KTB>;
   using GB = Geom<EB, LB, RB_ROWS, KTB>;
@@ -109,8 +130,8 @@ __global__ __launch_bounds__(THREADS) void gemm_stream_kernel(DenseArgs p) {
   using frag_t = typename Op::frag_t;
   constexpr int STAGE = GA::BYTES + GB::BYTES;
   constexpr int IPS = LdA::INSTR + LdB::INSTR;  // DMA instructions per wave and stage
-  static_assert(NS * STAGE <= LDS_RING && NS >= 3, "ring");
-  static_assert((NS - 2) * IPS < 64, "vmcnt counts at most 63 instructions");
+  static_assert(NS * STAGE <= LDS_RING && NG >= 3, "ring");
+  static_assert((NS - U) * IPS < 64, "vmcnt counts at most 63 instructions");
   static_assert(RBLK * KG == NW, "wave arrangement");
 
   __shared__ __attribute__((aligned(1024))) char smem_raw[NS * STAGE];
@@ -130,11 +151,11 @@ __global__ __launch_bounds__(THREADS) void gemm_stream_kernel(DenseArgs p) {
   if constexpr (LA == LAYOUT_K)
     la.init(p.A + m0 * p.lda * EB, (uint32_t)(min(p.M - m0, (int64_t)RA_ROWS) * p.lda * EB), p.lda, p.K, wave, lane);
   else
-    la.init(p.A + m0 * EB, (uint32_t)((p.K * p.lda - m0) * EB), p.lda, p.K, wave, lane);
+    la.init(p.A + m0 * EB, mn_window(p.K, p.lda, p.M, m0, EB), p.lda, p.K, wave, lane);
   if constexpr (LB == LAYOUT_K)
     lb.init(p.B + n0 * p.ldb * EB, (uint32_t)(min(p.N - n0, (int64_t)RB_ROWS) * p.ldb * EB), p.ldb, p.K, wave, lane);
   else
-    lb.init(p.B + n0 * EB, (uint32_t)((p.K * p.ldb - n0) * EB), p.ldb, p.K, wave, lane);
+    lb.init(p.B + n0 * EB, mn_window(p.K, p.ldb, p.N, n0, EB), p.ldb, p.K, wave, lane);
 
   // this workgroup's K tiles: [kt0, kt0 + nkl)
   const int nk_all = (int)((p.K + KTB / EB - 1) / (KTB / EB));
@@ -160,29 +181,34 @@ __global__ __launch_bounds__(THREADS) void gemm_stream_kernel(DenseArgs p) {
 
   acc_t acc{};
 #pragma unroll
-  for (int t = 0; t < NS - 1; ++t) issue(t);
-  for (int t = 0; t < nkl; ++t) {
-    wait_vmcnt<(NS - 2) * IPS>();  // this wave's part of tile t has landed
-    barrier_lds();                 // ... and every wave's; stage of tile t - 1 is free
-    issue(t + NS - 1);
-    const lds_char* sA = stage(t);
-    const lds_char* sB = sA + GA::BYTES;
-    // instruction s of the stage goes to K group (t * SPS + s) mod KG
+  for (int t = 0; t < NS - U; ++t) issue(t);
+  for (int t0 = 0; t0 < nkl; t0 += U) {
+    wait_vmcnt<(NS - 2 * U) * IPS>();  // this wave's part of tiles t0 .. t0 + U - 1 has landed
+    barrier_lds();                     // ... and every wave's; the stages of the U tiles before are free
 #pragma unroll
-    for (int s = 0; s < SPS; ++s) {
-      if (KG > 1 && (t * SPS + s) % KG != kg) continue;
-      const int kb = 2 * LB16 * s + LB16 * g;  // lane group g's K bytes of instruction s
-      // a K-contiguous operand's ordinary reads go before the other's asm block,
-      // whose wait then covers them
-      frag_t fa, fb;
-      if constexpr (LA == LAYOUT_K || LB == LAYOUT_MN) {
-        fa = StreamFrag<Op, RdA, LA, RA_ROWS * EB>::read(sA, rbA, kb, lane);
-        fb = StreamFrag<Op, RdB, LB, RB_ROWS * EB>::read(sB, rbB, kb, lane);
-      } else {
-        fb = StreamFrag<Op, RdB, LB, RB_ROWS * EB>::read(sB, rbB, kb, lane);
-        fa = StreamFrag<Op, RdA, LA, RA_ROWS * EB>::read(sA, rbA, kb, lane);
+    for (int u = 0; u < U; ++u) issue(t0 + NS - U + u);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {  // (tiles past the range are zeros)
+      const int t = t0 + u;
+      const lds_char* sA = stage(t);
+      const lds_char* sB = sA + GA::BYTES;
+      // instruction s of the stage goes to K group (t * SPS + s) mod KG
+#pragma unroll
+      for (int s = 0; s < SPS; ++s) {
+        if (KG > 1 && (t * SPS + s) % KG != kg) continue;
+        const int kb = 2 * LB16 * s + LB16 * g;  // lane group g's K bytes of instruction s
+        // a K-contiguous operand's ordinary reads go before the other's asm block,
+        // whose wait then covers them
+        frag_t fa, fb;
+        if constexpr (LA == LAYOUT_K || LB == LAYOUT_MN) {
+          fa = StreamFrag<Op, RdA, LA, RA_ROWS * EB>::read(sA, rbA, kb, lane);
+          fb = StreamFrag<Op, RdB, LB, RB_ROWS * EB>::read(sB, rbB, kb, lane);
+        } else {
+          fb = StreamFrag<Op, RdB, LB, RB_ROWS * EB>::read(sB, rbB, kb, lane);
+          fa = StreamFrag<Op, RdA, LA, RA_ROWS * EB>::read(sA, rbA, kb, lane);
+        }
+        Op::mma(acc, fb, fa);
       }
-      Op::mma(acc, fb, fa);
     }
   }
   wait_vmcnt<0>();  // no LDS DMA outstanding at exit
@@ -223,6 +249,18 @@ __global__ __launch_bounds__(THREADS) void gemm_stream_kernel(DenseArgs p) {
   const int64_t m = m0 + rbA + ACC::coord(lane, 0).j;
   if (m >= p.M) return;
   const int64_t nb = n0 + rbB + ACC::coord(lane, 0).i;
+  if constexpr (std::is_same<Op, I8Scaled>::value) {
+    const float sa = p.splits > 1 ? 0.0f : p.sa[m];
+#pragma unroll
+    for (int r4 = 0; r4 < 4; ++r4) {
+      const int64_t n = nb + 8 * r4;
+      if (n >= p.N) continue;
+      const i32x4 v = {acc[4 * r4], acc[4 * r4 + 1], acc[4 * r4 + 2], acc[4 * r4 + 3]};
+      if (p.splits > 1) scaled_part4(p, blockIdx.y, m, n, v);
+      else scaled_store4(p, m, n, v, sa);
+    }
+    return;
+  } else {
   if (gridDim.y > 1) {
     // split K: add alpha * partial sum into the zeroed D
 #pragma unroll
@@ -273,10 +311,11 @@ __global__ __launch_bounds__(THREADS) void gemm_stream_kernel(DenseArgs p) {
         if (n + e < p.N) combine_store(p.C, p.D, off + e, acc[4 * r4 + e], p.alpha, p.beta, p.use_c, p.out);
     }
   }
+  }
 }
 
 template <class Op, int LA, int LB, bool WIDE_A>
-static hipError_t launch_one(const DenseArgs& a, hipStream_t s) {
+static hipError_t launch_one(const typename StreamArgs<Op>::type& a, hipStream_t s) {
   const int64_t wide = WIDE_A ? a.M : a.N;
   const int bw = a.stream_bw;
   const int64_t blocks = (wide + bw - 1) / bw;
@@ -338,6 +377,11 @@ hipError_t launch_stream(int dtA, int dtB, int la, int lb, const DenseArgs& a, h
   const bool wide_a = a.N <= stream::NR && a.N <= a.M;
   return wide_a ? stream::launch_ops<true>(dtA, dtB, la, lb, a, s)
                 : stream::launch_ops<false>(dtA, dtB, la, lb, a, s);
+}
+
+hipError_t launch_scaled_stream(int layoutB, const ScaledArgs& a, hipStream_t s) {
+  return layoutB == LAYOUT_K ? stream::launch_one<stream::I8Scaled, LAYOUT_K, LAYOUT_K, false>(a, s)
+                             : stream::launch_one<stream::I8Scaled, LAYOUT_K, LAYOUT_MN, false>(a, s);
 }
 
 }  // namespace mcg

@@ -339,6 +339,26 @@ def test_gemm_i8_scaled_result_does_not_depend_on_the_workspace():
             assert torch.equal(run_scaled(mcg, a, sa, b, sb, None, "f32", "k_contig", ws=ws), base), (M, N, K, nb)
 
 
+@pytest.mark.parametrize("layoutB", ["k_contig", "mn_contig"])
+@pytest.mark.parametrize("shape", [(600, 1300, 2050), (1300, 700, 1999), (200, 3001, 4500)], ids=str)
+def test_gemm_i8_scaled_unaligned_operands_in_panels(layoutB, shape):
+    # operands without 16-byte chunks on the copies in the workspace, whole and in panels:
+    # the sums are exact, so every way gives the same bits
+    mcg = need_gpu()
+    M, N, K = shape
+    a, b = ref.codes(1, M, K), ref.codes(2, K, N)
+    sa, sb = ref.rand(3, M).abs().float() + 0.1, ref.rand(4, N).abs().float() + 0.1
+    bias = ref.rand(5, N).float()
+    pads = (5, 7, 3)
+    base = run_scaled(mcg, a, sa, b, sb, bias, "f32", layoutB, pads, 1)
+    d = ref.i8_scaled(a, sa, b, sb, bias)
+    within(base, d, scaled_tol(d, d - bias.double(), bias, "f32"), f"{layoutB} {shape}")
+    copy = (M + 512) * (K + 16) + 4096
+    for nb in (copy, copy + 300 * (K + 16), 64 << 20):
+        ws = torch.full((nb,), 0x7B, dtype=torch.uint8, device="cuda")
+        assert torch.equal(run_scaled(mcg, a, sa, b, sb, bias, "f32", layoutB, pads, 1, ws), base), nb
+
+
 GRAD_SHAPES = [(1, 1, 1), (3, 5, 7), (64, 64, 64), (100, 130, 257), (128, 128, 4096), (129, 255, 1000), (256, 512, 333), (300, 300, 2),
                (256, 256, 2048), (512, 384, 640), (520, 776, 1032), (1, 1000, 500), (1000, 1, 300)]
 
@@ -375,6 +395,43 @@ def test_gemm_grad_i8(dtA, layoutA, shape):
             mcg.gemm_grad_i8(dtA, layoutA, M, N, K, A, ld(A), Q, ld(Q), s.cuda(), C, C, ld(C), dtD, beta, w)
             torch.cuda.synchronize()
             assert torch.equal(C, D)
+
+
+def grad_tol(dtA, dtD, a, s, d, mag, K):
+    """As in test_gemm_grad_i8, with one more binary32 rounding for a result added up
+    from two products."""
+    operand = U[dtA] if dtD != "f32" else U[dtA] ** 2
+    near0 = SUB[dtA] * (a.double().abs().sum(1, keepdim=True))
+    tol = (operand + (4 * (K + 2) + 1) * U32) * mag + near0 + 4 * U32 * d.abs()
+    return tol if dtD == "f32" else tol + U[dtD] * (d.abs() + tol) + SUB[dtD]
+
+
+@pytest.mark.parametrize("dtA", ["bf16", "f16"])
+@pytest.mark.parametrize("layoutA", ["k_contig", "mn_contig"])
+@pytest.mark.parametrize("shape", [(512, 1536, 4096), (515, 1545, 4099), (90, 2000, 3000)], ids=str)
+def test_gemm_grad_i8_in_panels(dtA, layoutA, shape):
+    # panels of the widened Q in the workspace: whole, cut along N, and with a copy of an A
+    # without 16-byte chunks
+    mcg = need_gpu()
+    M, N, K = shape
+    a = ref.rand(K, M, K).to(DT[dtA])
+    q, s = ref.codes(K + 1, K, N), ref.rand(K + 2, K).abs().float() * 0.02 + 1e-3
+    core, mag = ref.grad_i8(a, q, s, None, 0.0)
+    c = ref.rand(K + 3, M, N)
+    for dtD, beta, pad in ((dtA, 0.0, 0), ("f32", 1.0, 0), ("f32", 0.0, 3), (dtA, -0.5, 5)):
+        A = put(a if layoutA == "k_contig" else a.T.contiguous(), pad)
+        Q = put(q, pad)
+        C = put(c.to(DT[dtD]), pad)
+        d = core + beta * c.to(DT[dtD]).double() if beta else core
+        full = mag + (abs(beta) * c.abs() if beta else 0)
+        two = 2 if dtD == "f32" else 1
+        copy = (M + 8) * (K + 8) * 2
+        for nb in (copy + 600 * (K + 8) * 2 * two, 64 << 20):
+            ws = torch.full((nb // 4,), float("nan"), device="cuda")
+            D = empty(M, N, DT[dtD], pad)
+            mcg.gemm_grad_i8(dtA, layoutA, M, N, K, A, ld(A), Q, ld(Q), s.cuda(), C if beta else None, D, ld(D), dtD, beta, ws)
+            guards_hold(D)
+            within(D, d, grad_tol(dtA, dtD, a, s, d, full, K), f"{dtA} -> {dtD} {layoutA} {shape} beta {beta} workspace {nb}")
 
 
 def test_gemm_grad_i8_empty_sum_and_marked_rows():

@@ -166,7 +166,12 @@ def test_workspace_queries():
     assert m.i8_scaled_workspace_bytes("k_contig", 0, 8, 8, FAKE, 8, FAKE, 8) == 0
     assert m.i8_scaled_workspace_bytes("k_contig", 8, 8, 200000, FAKE, 200000, FAKE, 200000) == 0
     assert m.i8_scaled_workspace_bytes("k_contig", 128, 256, 16384, FAKE, 16384, FAKE, 16384) > 0
-    assert m.grad_i8_workspace_bytes("bf16", "mn_contig", 8192, 8192, 8192, FAKE, 8192, FAKE, 8192, "bf16") == 0
+    # Q widened once: a panel of all its columns (two for a binary32 result)
+    one = 8192 * 8192 * 2
+    assert m.grad_i8_workspace_bytes("bf16", "mn_contig", 8192, 8192, 8192, FAKE, 8192, FAKE, 8192, "bf16") == one
+    assert m.grad_i8_workspace_bytes("bf16", "mn_contig", 8192, 8192, 8192, FAKE, 8192, FAKE, 8192, "f32") == 2 * one
+    # operands without 16-byte chunks: copies of both
+    assert m.i8_scaled_workspace_bytes("k_contig", 4000, 4001, 4003, FAKE, 4003, FAKE, 4003) >= (4000 + 4001) * 4016
     assert m.grad_i8_workspace_bytes("bf16", "mn_contig", 256, 256, 8192, FAKE, 256, FAKE, 256, "f32") > 0
     assert m.grad_i8_workspace_bytes("f32", "mn_contig", 256, 256, 8192, FAKE, 256, FAKE, 256, "f32") == 0
 
