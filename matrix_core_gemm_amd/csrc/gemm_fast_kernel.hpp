@@ -442,7 +442,9 @@ void gemm_fast_kernel(typename KernelTypes<Op>::Args p) {
     }
     return o;
   };
-  if (vec_ok && em0 + BM <= d.M && en0 + BN <= d.N) {
+  bool by_rows = vec_ok && em0 + BM <= d.M && en0 + BN <= d.N;
+  if constexpr (SCALED) by_rows = by_rows || d.sa;  // (checks the bounds itself)
+  if (by_rows) {
     // Interior tile.  Each wavefront passes the 32 x 64 block of its row group i
     // (KS: the one block it stores) through LDS (8 KiB; two buffers for the 256 x 256
     // form, one for the 128 x 128 form), so that 16 lanes then read C and write D
@@ -493,12 +495,7 @@ void gemm_fast_kernel(typename KernelTypes<Op>::Args p) {
     };
     if constexpr (SCALED) {
       if (d.sa) {
-        float sb[4], bias[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sb[e] = d.sb[col + e];
-          bias[e] = d.bias ? d.bias[col + e] : 0.0f;
-        }
+        const ScaledCols cols = scaled_cols(p, min(col, d.N - 1));
 #pragma unroll
         for (int i = 0; i < WTM; ++i) {
           __builtin_amdgcn_sched_barrier(0);
@@ -506,16 +503,12 @@ void gemm_fast_kernel(typename KernelTypes<Op>::Args p) {
           const int64_t row0 = em0 + rbA + 32 * i + rr;
           float sa[8];
 #pragma unroll
-          for (int t = 0; t < 8; ++t) sa[t] = d.sa[row0 + 4 * t];
+          for (int t = 0; t < 8; ++t) sa[t] = d.sa[min(row0 + 4 * t, d.M - 1)];
           v4 a[8];
           through_lds(i, wbuf + (KS ? 0 : (i & 1) * 8192), a, [] {});
 #pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            float o[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = scaled_value(a[t][e], sa[t], sb[e], bias[e]);
-            scaled_put4(d.D, (row0 + 4 * t) * d.ld + col, out, o, true, 4);
-          }
+          for (int t = 0; t < 8; ++t)
+            if (row0 + 4 * t < d.M && col < d.N) scaled_store4(p, row0 + 4 * t, col, a[t], sa[t], cols);
         }
         return;
       }
@@ -629,30 +622,6 @@ void gemm_fast_kernel(typename KernelTypes<Op>::Args p) {
               for (int r = 0; r < 4; ++r)
                 if (n + r < d.N) D16[off + r] = (uint16_t)to_out_bits(out, o[r]);
             }
-          }
-      }
-      return;
-    }
-  }
-  if constexpr (SCALED) {
-    if (d.sa) {
-#pragma unroll
-      for (int i = 0; i < WTM; ++i) {
-        __builtin_amdgcn_sched_barrier(0);
-        if (KS && i != grp) continue;  // the partner wave stores this row block
-        const int64_t m = em0 + rbA + 32 * i + acc_m;
-        if (m >= d.M) continue;
-        const float sa = d.sa[m];
-#pragma unroll
-        for (int j = 0; j < WTN; ++j)
-#pragma unroll
-          for (int r4 = 0; r4 < 4; ++r4) {
-            const int64_t n = en0 + rbB + 32 * j + acc_n(r4);
-            if (n >= d.N) continue;
-            i32x4 v;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = acc[i][j][4 * r4 + r];
-            scaled_store4(p, m, n, v, sa);
           }
       }
       return;
@@ -783,7 +752,7 @@ __global__ __launch_bounds__(256) void streamk_fixup_kernel(Args p, int64_t nk) 
       }
   }
   if constexpr (std::is_same<Args, ScaledArgs>::value) {
-    scaled_store4(p, m, n, acc, p.sa[m]);
+    scaled_store4(p, m, n, acc, p.sa[m], scaled_cols(p, n));
     return;
   } else {
   const int64_t doff = m * p.ldc + n;

@@ -18,8 +18,8 @@
 //     the operand's rounding.
 // Sums are binary32.
 //
-// General kernel: 128 x 128 tiles, 4 wavefronts, any size, pointer and leading
-// dimension.  Q's tile is widened on its way from the registers to LDS, where it is
+// General kernel: tiles of 128, 64 or 32 rows x 128 columns, 4 wavefronts, any size,
+// pointer and leading dimension.  Q's tile is widened on its way from the registers to LDS, where it is
 // an ordinary 16-bit MN-contiguous tile.
 #include <algorithm>
 
@@ -81,19 +81,20 @@ __device__ __forceinline__ void grad_store4(const GradArgs& p, int64_t m, int64_
   }
 }
 
-template <class Op, int LA, bool TWO>
-__global__ __launch_bounds__(256) void grad_general_kernel(GradArgs p) {
-  constexpr int BM = 128, BN = 128, NT = 256, WT = 4, KE = KT_BYTES / 2;
+template <class Op, int LA, bool TWO, int BM>
+__global__ __launch_bounds__(256, TWO && BM == 128 ? 1 : 2) void grad_general_kernel(GradArgs p) {
+  constexpr int BN = 128, NT = 256, KE = KT_BYTES / 2;
+  using WG = WaveGrid<BM>;
+  constexpr int WTM = WG::WTM, WTN = WG::WTN;
   using GA = TileGeom<2, LA, BM>;
   using GB = TileGeom<2, LAYOUT_MN, BN>;
   using RA = FragReader<2, 16, LA, BM>;
   using RB = FragReader<2, 16, LAYOUT_MN, BN>;
   constexpr int STAGE = GA::BYTES + (TWO ? 2 : 1) * GB::BYTES;
-  constexpr int QCPR = BN / 16, QPT = KE * QCPR / NT;  // 16-code chunks per row and per thread
   __shared__ __attribute__((aligned(16))) char smem_raw[2 * STAGE];
   lds_char* smem = (lds_char*)smem_raw;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave >> 1, wn = wave & 1;
+  const int rm = WG::row(wave), rn = WG::col(wave);
   int tm, tn;
   general_tile(blockIdx.x, p.tiles_m, p.tiles_n, tm, tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
@@ -101,31 +102,39 @@ __global__ __launch_bounds__(256) void grad_general_kernel(GradArgs p) {
   const int kt0 = (int)blockIdx.y * p.kt_per_split;
   const int nk = min(nk_all - kt0, p.kt_per_split);
 
-  AnyLoader<2, LA, BM, NT> la;
-  i32x4 q[QPT];
-  float s[QPT];
-  auto load_tiles = [&](int kt) {
-    const int64_t k0 = (int64_t)(kt0 + kt) * KE;
-    if constexpr (LA == LAYOUT_K) la.load(p.A, p.lda, m0, k0, p.M, p.K, tid);
-    else la.load(p.A, p.lda, k0, m0, p.K, p.M, tid);
+  // Two K tiles ahead in registers, two stages in LDS (see gemm_i8_scaled.hip).
+  using LdA = AnyLoader<2, LA, BM, NT>;
+  using LdQ = AnyLoader<1, LAYOUT_MN, BN, NT, KE>;
+  constexpr int QPT = LdQ::PER_THREAD;
+  LdA la;
+  LdQ lq;
+  la.init(p.A, p.lda, m0, p.M, p.K, tid);
+  lq.init(p.Q, p.ldq, n0, p.N, p.K, tid);
+  typename LdA::Regs ra[2];
+  typename LdQ::Regs q[2];
+  float sk[2][QPT];
+  auto load_tile = [&](auto set_c, int kt) {
+    constexpr int set = decltype(set_c)::value;
+    la.load(ra[set], kt0 + kt, kt < nk);
+    lq.load(q[set], kt0 + kt, kt < nk);
+    const global_f32* src = (const global_f32*)(kt < nk ? p.sk + (int64_t)(kt0 + kt) * KE : (const float*)load_nothing);
+    const int top = kt < nk ? lq.rows(kt0 + kt) - 1 : 0;  // (rows past K: their codes are zero)
 #pragma unroll
-    for (int t = 0; t < QPT; ++t) {
-      const int c = tid + t * NT;
-      const int64_t k = k0 + c / QCPR, n = n0 + 16 * (c % QCPR);
-      q[t] = load_chunk(p.Q, p.Q + k * p.ldq + n, k < p.K ? p.N - n : 0);
-      s[t] = k < p.K ? p.sk[k] : 0.0f;
-    }
+    for (int t = 0; t < QPT; ++t) sk[set][t] = src[min(lq.r0 + t * LdQ::RPI, top)];
   };
-  auto store_tiles = [&](lds_char* st) {
-    la.store(st, tid);
+  auto store_tile = [&](auto set_c, int kt) {
+    constexpr int set = decltype(set_c)::value;
+    lds_char* st = smem + set * STAGE;
+    la.settle(ra[set], kt0 + kt);
+    lq.settle(q[set], kt0 + kt);
+    la.store(ra[set], st);
     lds_char* tb = st + GA::BYTES;
 #pragma unroll
     for (int t = 0; t < QPT; ++t) {
-      const int c = tid + t * NT;
-      const int r = c / QCPR, cc = 2 * (c % QCPR);
+      const int r = lq.r0 + t * LdQ::RPI, cc = lq.c16 / 8;  // a chunk of codes widens to two
       const int sw = swz<2, LAYOUT_MN, GB::CPR>(r);
       i32x4 hi[2], lo[2];
-      widen16<Op, TWO>(q[t], s[t], hi, lo);
+      widen16<Op, TWO>(q[set][t], sk[set][t], hi, lo);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         lds_write_b128(tb, r * GB::W + (((cc + h) ^ sw) * 16), hi[h]);
@@ -133,55 +142,82 @@ __global__ __launch_bounds__(256) void grad_general_kernel(GradArgs p) {
       }
     }
   };
-  f32x4 acc[WT][WT];
+  f32x4 acc[WTM][WTN];
 #pragma unroll
-  for (int i = 0; i < WT; ++i)
+  for (int i = 0; i < WTM; ++i)
 #pragma unroll
-    for (int j = 0; j < WT; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  if (nk > 0) {
-    load_tiles(0);
-    store_tiles(smem);
-    __syncthreads();
-  }
-  for (int kt = 0; kt < nk; ++kt) {
-    lds_char* cur = smem + (kt & 1) * STAGE;
-    if (kt + 1 < nk) load_tiles(kt + 1);
+    for (int j = 0; j < WTN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  auto step = [&](auto cur_c, int kt) {
+    constexpr int set = decltype(cur_c)::value;
+    lds_char* cur = smem + set * STAGE;
+    store_tile(std::integral_constant<int, set ^ 1>{}, kt + 1);
+    load_tile(std::integral_constant<int, set ^ 1>{}, kt + 3);
 #pragma unroll
     for (int st = 0; st < Op::STEPS; ++st) {
-      i32x4 fa[WT], fb[WT];
+      i32x4 fa[WTM], fb[WTN];
 #pragma unroll
-      for (int i = 0; i < WT; ++i) fa[i] = RA::read(cur, wm * 64 + i * 16, st, lane);
+      for (int i = 0; i < WTM; ++i) fa[i] = RA::read(cur, rm + i * 16, st, lane);
 #pragma unroll
       for (int h = 0; h < (TWO ? 2 : 1); ++h) {
 #pragma unroll
-        for (int j = 0; j < WT; ++j) fb[j] = RB::read(cur + GA::BYTES + h * GB::BYTES, wn * 64 + j * 16, st, lane);
+        for (int j = 0; j < WTN; ++j) fb[j] = RB::read(cur + GA::BYTES + h * GB::BYTES, rn + j * 16, st, lane);
 #pragma unroll
-        for (int i = 0; i < WT; ++i)
+        for (int i = 0; i < WTM; ++i)
 #pragma unroll
-          for (int j = 0; j < WT; ++j) acc[i][j] = Op::mma(fb[j], fa[i], acc[i][j]);
+          for (int j = 0; j < WTN; ++j) acc[i][j] = Op::mma(fb[j], fa[i], acc[i][j]);
       }
     }
-    if (kt + 1 < nk) store_tiles(smem + ((kt & 1) ^ 1) * STAGE);
-    __syncthreads();
+    barrier_tiles();
+  };
+  constexpr std::integral_constant<int, 0> even;
+  constexpr std::integral_constant<int, 1> odd;
+  load_tile(even, 0);
+  load_tile(odd, 1);
+  store_tile(even, 0);
+  load_tile(even, 2);
+  barrier_tiles();
+  int kt = 0;
+  for (; kt + 2 <= nk; kt += 2) {
+    step(even, kt);
+    step(odd, kt + 1);
   }
-  using ACC = frag::Acc<frag::ACC_16x16>;
-  const int acc_m = ACC::coord(lane, 0).j, acc_n = ACC::coord(lane, 0).i;
-#pragma unroll
-  for (int i = 0; i < WT; ++i) {
-    const int64_t m = m0 + wm * 64 + i * 16 + acc_m;
-    if (m >= p.M) continue;
-#pragma unroll
-    for (int j = 0; j < WT; ++j) {
-      const int64_t n = n0 + wn * 64 + j * 16 + acc_n;
-      if (n >= p.N) continue;
-      if (p.splits > 1) {
-        float* w = (float*)p.ws + ((int64_t)blockIdx.y * p.M + m) * p.N + n;
-        for (int e = 0; e < 4; ++e)
-          if (n + e < p.N) w[e] = acc[i][j][e];
-      } else {
-        grad_store4(p, m, n, acc[i][j]);
-      }
+  if (kt < nk) step(even, kt);
+  static_assert(BM * 512 <= 2 * STAGE, "epilogue stage");
+  store_tile_rows<WG, BM>(smem, acc, tid, [&](int r, int c, const f32x4& v) {
+    const int64_t m = m0 + r, n = n0 + c;
+    if (m >= p.M || n >= p.N) return;
+    if (p.splits == 1) {
+      grad_store4(p, m, n, v);
+      return;
     }
+    float* w = (float*)p.ws + ((int64_t)blockIdx.y * p.M + m) * p.N + n;
+    if (p.N % 4 == 0) *(f32x4*)w = v;
+    else
+      for (int e = 0; e < 4; ++e)
+        if (n + e < p.N) w[e] = v[e];
+  });
+}
+
+// Operands of fewer than 16 bytes, which the general kernel's loads do not take, and
+// empty sums: one output per thread, the values rounded as elsewhere.
+template <class Op, int LA, bool TWO>
+__global__ __launch_bounds__(256) void grad_tiny_kernel(GradArgs p) {
+  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (n >= p.N) return;
+  auto value = [](const i32x4 (&v)[2]) {
+    const uint32_t b = (uint32_t)v[0][0] & 0xffffu;
+    return std::is_same<Op, OpBF16>::value ? bit_cast<float>(b << 16) : f16_bits_to_f32(b);
+  };
+  for (int64_t m = blockIdx.y; m < p.M; m += gridDim.y) {
+    float acc = 0.0f;
+    for (int64_t k = 0; k < p.K; ++k) {
+      i32x4 hi[2], lo[2];
+      widen16<Op, TWO>(i32x4{(int)(uint8_t)p.Q[k * p.ldq + n], 0, 0, 0}, p.sk[k], hi, lo);
+      const i32x4 bits[2] = {i32x4{(int)((const uint16_t*)p.A)[LA == LAYOUT_K ? m * p.lda + k : k * p.lda + m], 0, 0, 0}, {}};
+      acc = __builtin_fmaf(value(bits), value(hi), acc);
+      if constexpr (TWO) acc = __builtin_fmaf(value(bits), value(lo), acc);
+    }
+    combine_store(p.C, p.D, m * p.ldd + n, acc, 1.0f, p.beta, p.use_c, p.out);
   }
 }
 
@@ -190,13 +226,7 @@ __global__ __launch_bounds__(256) void grad_finish_kernel(GradArgs p) {
   const int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (n >= p.N) return;
   for (int64_t m = blockIdx.y; m < p.M; m += gridDim.y) {
-    f32x4 acc = {0, 0, 0, 0};
-    for (int s = 0; s < p.splits; ++s) {
-      const float* w = (const float*)p.ws + ((int64_t)s * p.M + m) * p.N + n;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (n + e < p.N) acc[e] += w[e];
-    }
+    const f32x4 acc = sum_ranges4<f32x4>((const float*)p.ws + m * p.N + n, p.M * p.N, p.splits, n, p.N);
     grad_store4(p, m, n, acc);
   }
 }
@@ -212,7 +242,7 @@ __global__ __launch_bounds__(256) void grad_widen_kernel(const char* Q, const fl
   const int64_t k = i / cpr, c = 16 * (int64_t)(i % cpr);
   const float s = k < K ? sk[k] : 0.0f;
   i32x4 h[2], l[2];
-  widen16<Op, TWO>(load_chunk(Q, Q + k * ldq + n0 + c, k < K ? nc - c : 0), s, h, l);
+  widen16<Op, TWO>(load_chunk(Q, Q + k * ldq + n0 + c, k < K ? (int)min(nc - c, (int64_t)16) : 0), s, h, l);
   char* d = hi + (k * ldw + c) * 2;
   *(i32x4*)d = h[0];
   *(i32x4*)(d + 16) = h[1];
@@ -224,6 +254,17 @@ __global__ __launch_bounds__(256) void grad_widen_kernel(const char* Q, const fl
 }
 
 namespace {
+// K tiles of 64 values of the general kernel (fitted from 1 to 300 rows, 1000 to 8192
+// columns and K 512 to 8192, K in 1 to 16 ranges)
+TileCost general_cost(int rows, bool two) {
+  if (two)
+    return rows == 32   ? TileCost{1.0, 0.65, 2, 3.0}
+           : rows == 64 ? TileCost{1.2, 0.8, 2, 4.0}
+                        : TileCost{1.5, 1.5, 1, 8.0};
+  return rows == 32   ? TileCost{0.75, 0.5, 4, 3.0}
+         : rows == 64 ? TileCost{0.85, 0.6, 3, 4.0}
+                      : TileCost{1.1, 0.78, 2, 8.0};
+}
 int64_t cdiv(int64_t x, int64_t y) { return (x + y - 1) / y; }
 int64_t round_up(int64_t x, int64_t y) { return cdiv(x, y) * y; }
 constexpr int64_t PANEL_STEP = 256;  // columns of a panel come in whole tiles
@@ -279,18 +320,27 @@ double plan_panels(int dtA, int la, GradArgs& a, int num_cu, int64_t ws_bytes, i
 // Two ways: the general kernel widens Q's tiles on their way to LDS, once for every
 // 128 rows of A, and takes any operands; panels widen Q once into the workspace (a
 // copy's time for 3 or 5 bytes an element) and multiply on the pipelined dense
-// kernels, at about half the time per product.  The modelled times decide: PANEL_NOTE
+// kernels, at about half the time per product.  The modelled times decide (bf16, in
+// place against panels: 64 x 4096 x 4096 21.2 and 33.5 us, 100 x 4096 x 4096 28.1 and
+// 31.4; 512^3 20.2 and 10.7, 4096^3 203 and 125, 8192^3 1480 and 873).
 int64_t plan_grad(int dtA, int la, GradArgs& a, int num_cu, int64_t ws_bytes) {
   const int64_t nk = cdiv(a.K, KT_BYTES / 2);
-  a.tiles_m = (int)cdiv(a.M, 128);
+  a.tile = general_rows(a.M);
+  a.tiles_m = (int)cdiv(a.M, a.tile);
   a.tiles_n = (int)cdiv(a.N, 128);
   const int64_t slot = a.M * a.N * 4;
   const int64_t most = slot > 0 ? ws_bytes / slot : 1;
   double general_us;
-  const int64_t s = plan_ranges((int64_t)a.tiles_m * a.tiles_n, nk, a.M * a.N, num_cu, a.out == OUT_32 ? 1.5 : 0.9,
-                                most < 64 ? most : 64, &general_us);
+  const int64_t s = plan_ranges((int64_t)a.tiles_m * a.tiles_n, nk, a.M * a.N, num_cu,
+                                general_cost(a.tile, a.out == OUT_32), most < 64 ? most : 64, &general_us);
   a.kt_per_split = (int)(nk > 0 ? cdiv(nk, s) : 1);
   a.splits = (int)s;
+  a.tiny = !any_operand_ok(2, la == LAYOUT_K ? a.M : a.K, la == LAYOUT_K ? a.K : a.M, a.lda) || !any_operand_ok(1, a.K, a.N, a.ldq);
+  if (a.tiny) {
+    a.panel_n = 0;
+    a.splits = 1;
+    return 0;
+  }
   if (a.K > 0) {
     int64_t used = 0;
     const double us = plan_panels(dtA, la, a, num_cu, ws_bytes, &used);
@@ -348,19 +398,42 @@ static hipError_t launch_panels(int dtA, int la, const GradArgs& a, int num_cu, 
 }
 
 template <class Op>
-static void launch_general(int la, const GradArgs& a, dim3 grid, hipStream_t s) {
+static void launch_tiny(int la, const GradArgs& a, hipStream_t s) {
+  const bool two = a.out == OUT_32;
+  const dim3 grid((unsigned)cdiv(a.N, 256), (unsigned)std::min<int64_t>(a.M, 65535));
+  if (la == LAYOUT_K) {
+    if (two) hipLaunchKernelGGL((grad_tiny_kernel<Op, LAYOUT_K, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((grad_tiny_kernel<Op, LAYOUT_K, false>), grid, dim3(256), 0, s, a);
+  } else {
+    if (two) hipLaunchKernelGGL((grad_tiny_kernel<Op, LAYOUT_MN, true>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((grad_tiny_kernel<Op, LAYOUT_MN, false>), grid, dim3(256), 0, s, a);
+  }
+}
+template <class Op, int BM>
+static void launch_rows(int la, const GradArgs& a, dim3 grid, hipStream_t s) {
   const bool two = a.out == OUT_32;
   if (la == LAYOUT_K) {
-    if (two) hipLaunchKernelGGL((grad_general_kernel<Op, LAYOUT_K, true>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((grad_general_kernel<Op, LAYOUT_K, false>), grid, dim3(256), 0, s, a);
+    if (two) hipLaunchKernelGGL((grad_general_kernel<Op, LAYOUT_K, true, BM>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((grad_general_kernel<Op, LAYOUT_K, false, BM>), grid, dim3(256), 0, s, a);
   } else {
-    if (two) hipLaunchKernelGGL((grad_general_kernel<Op, LAYOUT_MN, true>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((grad_general_kernel<Op, LAYOUT_MN, false>), grid, dim3(256), 0, s, a);
+    if (two) hipLaunchKernelGGL((grad_general_kernel<Op, LAYOUT_MN, true, BM>), grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((grad_general_kernel<Op, LAYOUT_MN, false, BM>), grid, dim3(256), 0, s, a);
   }
+}
+template <class Op>
+static void launch_general(int la, const GradArgs& a, dim3 grid, hipStream_t s) {
+  if (a.tile == 32) launch_rows<Op, 32>(la, a, grid, s);
+  else if (a.tile == 64) launch_rows<Op, 64>(la, a, grid, s);
+  else launch_rows<Op, 128>(la, a, grid, s);
 }
 
 hipError_t launch_grad(int dtA, int layoutA, const GradArgs& a, int num_cu, hipStream_t s) {
   if (a.panel_n > 0) return launch_panels(dtA, layoutA, a, num_cu, s);
+  if (a.tiny) {
+    if (dtA == DT_BF16) launch_tiny<OpBF16>(layoutA, a, s);
+    else launch_tiny<OpF16>(layoutA, a, s);
+    return hipGetLastError();
+  }
   const int64_t blocks = (int64_t)a.tiles_m * a.tiles_n;
   if (blocks > 0xffffff) return hipErrorInvalidValue;  // (a launch holds less than 2^32 threads)
   const dim3 grid((unsigned)blocks, (unsigned)a.splits);

@@ -5,8 +5,8 @@
 // it cannot wrap); it is rounded once to binary32, multiplied by sa and by sb,
 // added to the bias and rounded to D's type.
 //
-// General kernel: 128 x 128 tiles, 4 wavefronts, any size, pointer and leading
-// dimension; the structure of dense_general.hpp with the loaders of tile_any.hpp.
+// General kernel: tiles of 128, 64 or 32 rows (general_rows) x 128 columns, 4
+// wavefronts, any size, pointer and leading dimension; the structure of dense_general.hpp with the loaders of tile_any.hpp.
 // K may be cut into ranges (few tiles, long K): each range leaves its int32 sums
 // in the workspace and a second kernel adds them and applies the epilogue.
 #include <algorithm>
@@ -16,9 +16,11 @@
 
 namespace mcg {
 
-template <int LB>
-__global__ __launch_bounds__(256) void scaled_general_kernel(ScaledArgs p) {
-  constexpr int BM = 128, BN = 128, NT = 256, WT = 4;
+template <int LB, int BM>
+__global__ __launch_bounds__(256, 2) void scaled_general_kernel(ScaledArgs p) {
+  constexpr int BN = 128, NT = 256;
+  using WG = WaveGrid<BM>;
+  constexpr int WTM = WG::WTM, WTN = WG::WTN;
   using Op = OpI8;
   using GA = TileGeom<1, LAYOUT_K, BM>;
   using GB = TileGeom<1, LB, BN>;
@@ -29,7 +31,7 @@ __global__ __launch_bounds__(256) void scaled_general_kernel(ScaledArgs p) {
   lds_char* ldsA[2] = {smem, smem + GA::BYTES + GB::BYTES};
   lds_char* ldsB[2] = {smem + GA::BYTES, smem + 2 * GA::BYTES + GB::BYTES};
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave >> 1, wn = wave & 1;
+  const int rm = WG::row(wave), rn = WG::col(wave);
   int tm, tn;
   general_tile(blockIdx.x, p.tiles_m, p.tiles_n, tm, tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
@@ -37,61 +39,91 @@ __global__ __launch_bounds__(256) void scaled_general_kernel(ScaledArgs p) {
   const int kt0 = (int)blockIdx.y * p.kt_per_split;
   const int nk = min(nk_all - kt0, p.kt_per_split);
 
-  AnyLoader<1, LAYOUT_K, BM, NT> la;
-  AnyLoader<1, LB, BN, NT> lb;
-  auto load_tiles = [&](int kt) {
-    const int64_t k0 = (int64_t)(kt0 + kt) * KT_BYTES;
-    la.load(p.A, p.lda, m0, k0, p.M, p.K, tid);
-    if constexpr (LB == LAYOUT_K) lb.load(p.B, p.ldb, n0, k0, p.N, p.K, tid);
-    else lb.load(p.B, p.ldb, k0, n0, p.K, p.N, tid);
+  // Two K tiles ahead in registers, two stages in LDS.  (One tile ahead, with loads the
+  // compiler waited for at the end of every condition around them: one token x 8000 x
+  // 8000, rows 8003 apart, 29 us; so 17.4, the streaming kernel's time for aligned rows.)
+  using LdA = AnyLoader<1, LAYOUT_K, BM, NT>;
+  using LdB = AnyLoader<1, LB, BN, NT>;
+  LdA la;
+  LdB lb;
+  la.init(p.A, p.lda, m0, p.M, p.K, tid);
+  lb.init(p.B, p.ldb, n0, p.N, p.K, tid);
+  typename LdA::Regs ra[2];
+  typename LdB::Regs rb[2];
+  auto load_tile = [&](auto set_c, int kt) {
+    constexpr int set = decltype(set_c)::value;
+    la.load(ra[set], kt0 + kt, kt < nk);
+    lb.load(rb[set], kt0 + kt, kt < nk);
   };
-  i32x4 acc[WT][WT];
+  auto store_tile = [&](auto set_c, int kt) {
+    constexpr int set = decltype(set_c)::value;
+    la.settle(ra[set], kt0 + kt);
+    lb.settle(rb[set], kt0 + kt);
+    la.store(ra[set], ldsA[set]);
+    lb.store(rb[set], ldsB[set]);
+  };
+  i32x4 acc[WTM][WTN];
 #pragma unroll
-  for (int i = 0; i < WT; ++i)
+  for (int i = 0; i < WTM; ++i)
 #pragma unroll
-    for (int j = 0; j < WT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-  if (nk > 0) {
-    load_tiles(0);
-    la.store(ldsA[0], tid);
-    lb.store(ldsB[0], tid);
-    __syncthreads();
-  }
-  for (int kt = 0; kt < nk; ++kt) {
-    const int cur = kt & 1;
-    if (kt + 1 < nk) load_tiles(kt + 1);
+    for (int j = 0; j < WTN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  // K tile kt in stage cur = kt % 2; tile kt + 1 goes from its registers to the other stage
+  auto step = [&](auto cur_c, int kt) {
+    constexpr int cur = decltype(cur_c)::value;
+    store_tile(std::integral_constant<int, cur ^ 1>{}, kt + 1);
+    load_tile(std::integral_constant<int, cur ^ 1>{}, kt + 3);
 #pragma unroll
     for (int s = 0; s < Op::STEPS; ++s) {
-      i32x4 fa[WT], fb[WT];
+      i32x4 fa[WTM], fb[WTN];
 #pragma unroll
-      for (int i = 0; i < WT; ++i) fa[i] = RA::read(ldsA[cur], wm * 64 + i * 16, s, lane);
+      for (int i = 0; i < WTM; ++i) fa[i] = RA::read(ldsA[cur], rm + i * 16, s, lane);
 #pragma unroll
-      for (int j = 0; j < WT; ++j) fb[j] = RB::read(ldsB[cur], wn * 64 + j * 16, s, lane);
+      for (int j = 0; j < WTN; ++j) fb[j] = RB::read(ldsB[cur], rn + j * 16, s, lane);
 #pragma unroll
-      for (int i = 0; i < WT; ++i)
+      for (int i = 0; i < WTM; ++i)
 #pragma unroll
-        for (int j = 0; j < WT; ++j) acc[i][j] = Op::mma(fb[j], fa[i], acc[i][j]);
+        for (int j = 0; j < WTN; ++j) acc[i][j] = Op::mma(fb[j], fa[i], acc[i][j]);
     }
-    if (kt + 1 < nk) {
-      la.store(ldsA[cur ^ 1], tid);
-      lb.store(ldsB[cur ^ 1], tid);
-    }
-    __syncthreads();
+    barrier_tiles();
+  };
+  constexpr std::integral_constant<int, 0> even;
+  constexpr std::integral_constant<int, 1> odd;
+  load_tile(even, 0);
+  load_tile(odd, 1);
+  store_tile(even, 0);
+  load_tile(even, 2);
+  barrier_tiles();
+  int kt = 0;
+  for (; kt + 2 <= nk; kt += 2) {
+    step(even, kt);
+    step(odd, kt + 1);
   }
-  // a lane holds 4 consecutive columns of one row of each 16 x 16 block
-  using ACC = frag::Acc<frag::ACC_16x16>;
-  const int acc_m = ACC::coord(lane, 0).j, acc_n = ACC::coord(lane, 0).i;
-#pragma unroll
-  for (int i = 0; i < WT; ++i) {
-    const int64_t m = m0 + wm * 64 + i * 16 + acc_m;
-    if (m >= p.M) continue;
-    const float sa = p.splits > 1 ? 0.0f : p.sa[m];
-#pragma unroll
-    for (int j = 0; j < WT; ++j) {
-      const int64_t n = n0 + wn * 64 + j * 16 + acc_n;
-      if (n >= p.N) continue;
-      if (p.splits > 1) scaled_part4(p, blockIdx.y, m, n, acc[i][j]);
-      else scaled_store4(p, m, n, acc[i][j], sa);
-    }
+  if (kt < nk) step(even, kt);
+  static_assert(BM * 512 <= 2 * (GA::BYTES + GB::BYTES), "epilogue stage");
+  if (p.splits > 1) {
+    store_tile_rows<WG, BM>(smem, acc, tid, [&](int r, int c, const i32x4& v) {
+      if (m0 + r < p.M && n0 + c < p.N) scaled_part4(p, blockIdx.y, m0 + r, n0 + c, v);
+    });
+    return;
+  }
+  const ScaledCols cols = scaled_cols(p, min(n0 + 4 * (tid & 31), p.N - 1));
+  store_tile_rows<WG, BM>(smem, acc, tid, [&](int r, int c, const i32x4& v) {
+    if (m0 + r < p.M && n0 + c < p.N) scaled_store4(p, m0 + r, n0 + c, v, p.sa[m0 + r], cols);
+  });
+}
+
+// Operands of fewer than 16 bytes, which the general kernel's loads do not take, and
+// empty sums: one output per thread.
+template <int LB>
+__global__ __launch_bounds__(256) void scaled_tiny_kernel(ScaledArgs p) {
+  const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (n >= p.N) return;
+  for (int64_t m = blockIdx.y; m < p.M; m += gridDim.y) {
+    int acc = 0;
+    for (int64_t k = 0; k < p.K; ++k)
+      acc += (int)(int8_t)p.A[m * p.lda + k] * (int)(int8_t)p.B[LB == LAYOUT_K ? n * p.ldb + k : k * p.ldb + n];
+    const float o[4] = {scaled_value(acc, p.sa[m], p.sb[n], p.bias ? p.bias[n] : 0.0f), 0, 0, 0};
+    scaled_put4(p.D, m * p.ldc + n, p.out, o, false, 1);
   }
 }
 
@@ -99,25 +131,21 @@ __global__ __launch_bounds__(256) void scaled_general_kernel(ScaledArgs p) {
 __global__ __launch_bounds__(256) void scaled_finish_kernel(ScaledArgs p) {
   const int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (n >= p.N) return;
+  const ScaledCols cols = scaled_cols(p, n);
   for (int64_t m = blockIdx.y; m < p.M; m += gridDim.y) {
-    i32x4 acc = {0, 0, 0, 0};
-    for (int s = 0; s < p.splits; ++s) {
-      const int32_t* w = (const int32_t*)p.ws + ((int64_t)s * p.M + m) * p.N + n;
-      if (p.N % 4 == 0) {
-        const i32x4 v = *(const i32x4*)w;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] += v[e];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n + e < p.N) acc[e] += w[e];
-      }
-    }
-    scaled_store4(p, m, n, acc, p.sa[m]);
+    const i32x4 acc = sum_ranges4<i32x4>((const int32_t*)p.ws + m * p.N + n, p.M * p.N, p.splits, n, p.N);
+    scaled_store4(p, m, n, acc, p.sa[m], cols);
   }
 }
 
 namespace {
+// K tiles of 128 values of the general kernel (fitted from 1 to 300 rows, 1000 to 8192
+// columns and K 512 to 8192, rows 3 bytes longer than K, K in 1 to 16 ranges)
+TileCost general_cost(int rows) {
+  return rows == 32   ? TileCost{0.65, 0.65, 4, 3.0}
+         : rows == 64 ? TileCost{0.85, 0.7, 3, 4.0}
+                      : TileCost{1.2, 0.8, 2, 5.0};
+}
 int64_t cdiv(int64_t x, int64_t y) { return (x + y - 1) / y; }
 int64_t round_up(int64_t x, int64_t y) { return cdiv(x, y) * y; }
 constexpr int64_t LIM = (int64_t)1 << 31;  // buffer offsets stay below it
@@ -130,8 +158,12 @@ bool chunks_ok(const ScaledArgs& a, int lb) {
   return a.K > 0 && a.K % 16 == 0 && a.lda % 16 == 0 && a.ldb % 16 == 0 && (uintptr_t)a.A % 16 == 0 &&
          (uintptr_t)a.B % 16 == 0 && offsets_ok(a.K, a.lda, lb, a.ldb);
 }
-// Streaming kernel: blocks of 32 channels until there are 64 per compute unit.
-constexpr int64_t STREAM_MIN_BLOCKS = 128, STREAM_MIN_KT = 16;
+// Streaming kernel.  A compute unit keeps about 20 bytes per ns of B in flight, so B
+// comes at HBM's rate only when every one has a block: the K ranges follow from
+//   rounds * K tiles * STREAM_KT_US * rows + [s > 1] (SUM_US + s * M * N trips of 8 bytes),
+// with at least STREAM_MIN_KT K tiles in a range.
+constexpr double STREAM_KT_US = 0.2 / 32, STREAM_SUM_US = 4.0;  // per row of a block and K tile
+constexpr int64_t STREAM_MIN_KT = 8;
 constexpr int64_t PANEL_STEP = 256;  // columns of a panel come in whole tiles
 
 // The pipelined problem on the copies of A and of a panel of B with nc columns.
@@ -173,10 +205,11 @@ double plan_panels(int lb, ScaledArgs& a, int num_cu, int64_t ws_bytes, int64_t*
 
 // Fills the plan's fields and returns the workspace bytes it takes (at most ws_bytes).
 //   - up to 32 rows in 16-byte chunks: the streaming kernel (reads B once);
-//   - more rows in 16-byte chunks: the pipelined kernel, whole tiles or stream-K;
-//   - other operands: the general kernel reads them in place at any alignment, or
-//     copies with 16-byte chunks go to the pipelined kernel; the modelled times
-//     decide: PANEL_NOTE
+//   - more rows: the pipelined kernel (whole tiles or stream-K; operands without
+//     16-byte chunks go there as copies), or the general kernel, which reads any
+//     operands in place and cuts K where there are few tiles; the modelled times
+//     decide (4096^3, rows 4099 apart: 145 us in place, 79 with copies; 64 x 4096 x 4096:
+//     14.7 and 28)
 int64_t plan_scaled(ScaledArgs& a, int lb, int num_cu, int64_t ws_bytes) {
   const int64_t nk = cdiv(a.K, KT_BYTES);
   const int64_t slot = a.M * a.N * 4;
@@ -190,34 +223,47 @@ int64_t plan_scaled(ScaledArgs& a, int lb, int num_cu, int64_t ws_bytes) {
     a.splits = (int)(nk > 0 ? cdiv(nk, a.kt_per_split) : 1);
     return a.splits > 1 ? a.splits * slot : 0;
   };
-  if (chunks_ok(a, lb)) {
-    if (a.M <= 32) {
-      a.kernel = KERNEL_STREAM;
-      a.stream_bw = a.N >= 64 * (int64_t)num_cu || lb == LAYOUT_MN ? 128 : 32;
-      const int64_t blocks = cdiv(a.N, a.stream_bw);
-      int64_t s = 1;
-      if (blocks < STREAM_MIN_BLOCKS)
-        s = std::max<int64_t>(1, std::min(cdiv(STREAM_MIN_BLOCKS, blocks), nk / STREAM_MIN_KT));
-      return ranges(std::max<int64_t>(1, std::min(s, most)));
+  if (a.M <= 32 && chunks_ok(a, lb)) {
+    a.kernel = KERNEL_STREAM;
+    a.stream_bw = a.N >= 64 * (int64_t)num_cu || lb == LAYOUT_MN ? 128 : 32;
+    const int64_t blocks = cdiv(a.N, a.stream_bw);
+    int64_t best = 1;
+    double best_us = 0.0;
+    for (int64_t s = 1; s == 1 || (s <= most && nk / s >= STREAM_MIN_KT); ++s) {
+      const double us = cdiv(blocks * s, num_cu) * cdiv(nk, s) * STREAM_KT_US * a.stream_bw +
+                        (s > 1 ? STREAM_SUM_US + 2.0 * s * slot / 4.5e6 : 0.0);
+      if (s == 1 || us < best_us) {
+        best = s;
+        best_us = us;
+      }
     }
-    const PipePlan pp = plan_pipe(DT_I8, a, num_cu, ws_bytes);
-    a.kernel = KERNEL_FAST;
-    a.tile = pp.tile;
-    return pp.ws;
+    return ranges(best);
   }
-  a.kernel = KERNEL_GENERAL;
-  a.tiles_m = (int)cdiv(a.M, 128);
-  a.tiles_n = (int)cdiv(a.N, 128);
+  const int rows = general_rows(a.M);
+  const int64_t tiles_m = cdiv(a.M, rows), tiles_n = cdiv(a.N, 128);
   double general_us;
-  const int64_t s = plan_ranges((int64_t)a.tiles_m * a.tiles_n, nk, a.M * a.N, num_cu, 1.0, most < 64 ? most : 64, &general_us);
-  if (a.K > 0) {
+  const int64_t s = plan_ranges(tiles_m * tiles_n, nk, a.M * a.N, num_cu, general_cost(rows), most < 64 ? most : 64, &general_us);
+  if (chunks_ok(a, lb)) {
+    const PipePlan pp = plan_pipe(DT_I8, a, num_cu, ws_bytes);
+    if (pp.us < general_us) {
+      a.kernel = KERNEL_FAST;
+      a.tile = pp.tile;
+      return pp.ws;
+    }
+  } else if (a.K > 0) {
     int64_t used = 0;
     const double us = plan_panels(lb, a, num_cu, ws_bytes, &used);
     if (us > 0.0 && us < general_us) return used;
-    a.panel_n = 0;
-    a.dp_tiles = a.sk_tiles = a.sk_wgs = 0;
   }
-  return ranges(s);
+  a.kernel = any_operand_ok(1, a.M, a.K, a.lda) && any_operand_ok(1, lb == LAYOUT_K ? a.N : a.K, lb == LAYOUT_K ? a.K : a.N, a.ldb)
+                 ? KERNEL_GENERAL
+                 : KERNEL_TINY;
+  a.panel_n = 0;
+  a.dp_tiles = a.sk_tiles = a.sk_wgs = 0;
+  a.tile = rows;
+  a.tiles_m = (int)tiles_m;
+  a.tiles_n = (int)tiles_n;
+  return ranges(a.kernel == KERNEL_TINY ? 1 : s);
 }
 
 static hipError_t launch_pipe(int lb, const ScaledArgs& a, hipStream_t s) {
@@ -240,18 +286,31 @@ static hipError_t launch_panels(int lb, const ScaledArgs& a, int num_cu, hipStre
   return e;
 }
 
+template <int BM>
+static void launch_general(int lb, const ScaledArgs& a, dim3 grid, hipStream_t s) {
+  if (lb == LAYOUT_K) hipLaunchKernelGGL((scaled_general_kernel<LAYOUT_K, BM>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((scaled_general_kernel<LAYOUT_MN, BM>), grid, dim3(256), 0, s, a);
+}
+
 hipError_t launch_scaled(int layoutB, const ScaledArgs& a, int num_cu, hipStream_t s) {
   if (a.panel_n > 0) return launch_panels(layoutB, a, num_cu, s);
   if (a.kernel == KERNEL_FAST) return launch_pipe(layoutB, a, s);
   hipError_t e;
+  if (a.kernel == KERNEL_TINY) {
+    const dim3 grid((unsigned)cdiv(a.N, 256), (unsigned)std::min<int64_t>(a.M, 65535));
+    if (layoutB == LAYOUT_K) hipLaunchKernelGGL(scaled_tiny_kernel<LAYOUT_K>, grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(scaled_tiny_kernel<LAYOUT_MN>, grid, dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
   if (a.kernel == KERNEL_STREAM) {
     e = launch_scaled_stream(layoutB, a, s);
   } else {
     const int64_t blocks = (int64_t)a.tiles_m * a.tiles_n;
     if (blocks > 0xffffff) return hipErrorInvalidValue;  // (a launch holds less than 2^32 threads)
     const dim3 grid((unsigned)blocks, (unsigned)a.splits);
-    if (layoutB == LAYOUT_K) hipLaunchKernelGGL((scaled_general_kernel<LAYOUT_K>), grid, dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((scaled_general_kernel<LAYOUT_MN>), grid, dim3(256), 0, s, a);
+    if (a.tile == 32) launch_general<32>(layoutB, a, grid, s);
+    else if (a.tile == 64) launch_general<64>(layoutB, a, grid, s);
+    else launch_general<128>(layoutB, a, grid, s);
     e = hipGetLastError();
   }
   if (e != hipSuccess || a.splits == 1) return e;

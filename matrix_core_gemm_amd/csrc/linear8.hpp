@@ -56,13 +56,14 @@ struct ScaledArgs : DenseArgs {
   const float* sa;    // M
   const float* sb;    // N
   const float* bias;  // N, or null
-  int kernel;         // KERNEL_GENERAL, KERNEL_STREAM, or KERNEL_FAST with
-  int tile;           // PipePlan's tile
+  int kernel;         // KERNEL_TINY, KERNEL_GENERAL, KERNEL_STREAM, or KERNEL_FAST with
+  int tile;           // PipePlan's tile; KERNEL_GENERAL: rows of a tile
   // copies of operands without 16-byte chunks, for the pipelined kernel: panels of
   // panel_n columns (0: no copies), K padded with zeros to kp
   int64_t panel_n, kp, ldb2;
   int64_t ws_bytes;
 };
+constexpr int KERNEL_TINY = 16;  // (beside the dense kernels' codes)
 int64_t plan_scaled(ScaledArgs& a, int layoutB, int num_cu, int64_t ws_bytes);
 hipError_t launch_scaled(int layoutB, const ScaledArgs& a, int num_cu, hipStream_t s);
 // The pipelined kernel with tile x tile tiles (256 or 128) and the streaming kernel (M <= 32).
@@ -84,6 +85,8 @@ struct GradArgs {
   int out;
   int vec_d;
   // general kernel (panel_n == 0)
+  int tiny;            // the form for operands of less than 16 bytes
+  int tile;            // rows of a tile
   int tiles_m, tiles_n;
   int splits, kt_per_split;  // splits > 1: ws holds one M x N binary32 matrix per range
   // panels of Q widened in the workspace, for the pipelined dense kernels
@@ -113,6 +116,6 @@ PipePlan plan_pipe(int dt, DenseArgs& a, int num_cu, int64_t ws_cap);
 hipError_t launch_align_rows(const void* src, int64_t lds, int64_t rows, int64_t row_bytes, void* dst, int64_t ldd,
                              int64_t rows_d, hipStream_t s);
 // Time of a pass that moves `bytes` at the rate of a copy, with its launch, in us.
-inline double pass_us(double bytes) { return 3.0 + bytes / 4.5e6; }
+inline double pass_us(double bytes) { return 3.0 + bytes / 5.5e6; }
 
 }  // namespace mcg

@@ -46,7 +46,7 @@ __global__ __launch_bounds__(256) void align_rows_kernel(const char* src, int64_
   if (i >= chunks) return;
   const uint32_t r = i / cpr, c = i % cpr;
   const int64_t left = r < rows ? row_bytes - 16 * (int64_t)c : 0;
-  *(i32x4*)(dst + r * ldd + 16 * (int64_t)c) = load_chunk(src, src + r * lds + 16 * (int64_t)c, left);
+  *(i32x4*)(dst + r * ldd + 16 * (int64_t)c) = load_chunk(src, src + r * lds + 16 * (int64_t)c, (int)min(left, (int64_t)16));
 }
 
 hipError_t launch_align_rows(const void* src, int64_t lds, int64_t rows, int64_t row_bytes, void* dst, int64_t ldd,

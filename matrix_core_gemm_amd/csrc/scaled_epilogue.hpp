@@ -30,14 +30,28 @@ __device__ __forceinline__ void scaled_put4(void* D, int64_t off, int out, const
         if (e < left) d[e] = (uint16_t)b[e];
   }
 }
-// Four consecutive outputs at (m, n); n + 4 may pass N.
-__device__ __forceinline__ void scaled_store4(const ScaledArgs& p, int64_t m, int64_t n, const i32x4& acc, float sa) {
-  float o[4];
+// The scales and biases of four consecutive columns; n + 4 may pass N.  Kernels that
+// store several blocks load these first: behind a store, which might overwrite them
+// for all the compiler knows, every block waits for its own loads (16 blocks: 10 us).
+struct ScaledCols {
+  float sb[4], bias[4];
+};
+__device__ __forceinline__ ScaledCols scaled_cols(const ScaledArgs& p, int64_t n) {
+  ScaledCols c;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const int64_t c = n + e < p.N ? n + e : p.N - 1;
-    o[e] = scaled_value(acc[e], sa, p.sb[c], p.bias ? p.bias[c] : 0.0f);
+    const int64_t i = n + e < p.N ? n + e : p.N - 1;
+    c.sb[e] = p.sb[i];
+    c.bias[e] = p.bias ? p.bias[i] : 0.0f;
   }
+  return c;
+}
+// Four consecutive outputs at (m, n); n + 4 may pass N.
+__device__ __forceinline__ void scaled_store4(const ScaledArgs& p, int64_t m, int64_t n, const i32x4& acc, float sa,
+                                              const ScaledCols& c) {
+  float o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = scaled_value(acc[e], sa, c.sb[e], c.bias[e]);
   scaled_put4(p.D, m * p.ldc + n, p.out, o, p.vec_cd && n + 4 <= p.N, p.N - n);
 }
 // Four consecutive sums of K range `range` to the workspace.
