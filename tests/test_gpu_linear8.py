@@ -340,7 +340,7 @@ def test_gemm_i8_scaled_result_does_not_depend_on_the_workspace():
 
 
 @pytest.mark.parametrize("layoutB", ["k_contig", "mn_contig"])
-@pytest.mark.parametrize("shape", [(600, 1300, 2050), (1300, 700, 1999), (200, 3001, 4500)], ids=str)
+@pytest.mark.parametrize("shape", [(600, 1300, 2050), (1300, 700, 1999), (1001, 2003, 3001)], ids=str)
 def test_gemm_i8_scaled_unaligned_operands_in_panels(layoutB, shape):
     # operands without 16-byte chunks on the copies in the workspace, whole and in panels:
     # the sums are exact, so every way gives the same bits
@@ -408,7 +408,7 @@ def grad_tol(dtA, dtD, a, s, d, mag, K):
 
 @pytest.mark.parametrize("dtA", ["bf16", "f16"])
 @pytest.mark.parametrize("layoutA", ["k_contig", "mn_contig"])
-@pytest.mark.parametrize("shape", [(512, 1536, 4096), (515, 1545, 4099), (90, 2000, 3000)], ids=str)
+@pytest.mark.parametrize("shape", [(512, 1536, 4096), (600, 900, 700), (1001, 1103, 901)], ids=str)
 def test_gemm_grad_i8_in_panels(dtA, layoutA, shape):
     # panels of the widened Q in the workspace: whole, cut along N, and with a copy of an A
     # without 16-byte chunks
@@ -452,6 +452,81 @@ def test_gemm_grad_i8_empty_sum_and_marked_rows():
     mcg.gemm_grad_i8("bf16", "k_contig", 20, 30, 69, put(a), 70, put(q), 30, s.cuda(), None, D, 30, "bf16")
     torch.cuda.synchronize()
     assert bool(torch.isfinite(D).all())
+
+
+@pytest.mark.parametrize("layoutB", ["k_contig", "mn_contig"])
+@pytest.mark.parametrize("shape", [(100, 70, 5), (40, 3, 9), (3, 300, 15), (17, 15, 300), (2, 7, 1), (5, 3, 40)], ids=str)
+def test_gemm_i8_scaled_rows_shorter_than_a_chunk(layoutB, shape):
+    # rows of fewer than 16 bytes, and whole operands of fewer
+    mcg = need_gpu()
+    M, N, K = shape
+    a, b = ref.codes(K, M, K), ref.codes(K + 1, K, N)
+    sa, sb, bias = ref.rand(1, M).abs().float() + 0.1, ref.rand(2, N).abs().float() + 0.1, ref.rand(3, N).float()
+    d = ref.i8_scaled(a, sa, b, sb, bias)
+    for pads, off in (((0, 0, 0), 0), ((1, 2, 3), 1), ((16, 16, 4), 0)):
+        D = run_scaled(mcg, a, sa, b, sb, bias, "f32", layoutB, pads, off, torch.empty(1 << 20, dtype=torch.uint8, device="cuda"))
+        within(D, d, scaled_tol(d, d - bias.double(), bias, "f32"), f"{layoutB} {shape} pads {pads}")
+
+
+@pytest.mark.parametrize("layoutA", ["k_contig", "mn_contig"])
+@pytest.mark.parametrize("shape", [(3, 200, 40), (100, 70, 5), (2, 300, 500), (5, 130, 3), (1, 15, 1), (7, 2, 1), (33, 9, 70), (1, 3, 200)], ids=str)
+def test_gemm_grad_i8_rows_shorter_than_a_chunk(layoutA, shape):
+    mcg = need_gpu()
+    M, N, K = shape
+    a = ref.rand(K, M, K).to(torch.bfloat16)
+    q, s = ref.codes(K + 1, K, N), ref.rand(K + 2, K).abs().float() * 0.02 + 1e-3
+    c = ref.rand(K + 3, M, N)
+    for dtD, beta, pad, off in (("bf16", 0.0, 0, 0), ("f32", -0.5, 3, 1), ("bf16", 1.0, 16, 0)):
+        A, Q, C = put(a if layoutA == "k_contig" else a.T.contiguous(), pad, off), put(q, pad, off), put(c.to(DT[dtD]), pad, off)
+        d, mag = ref.grad_i8(a, q, s, c.to(DT[dtD]) if beta else None, beta)
+        if beta:
+            mag = mag + abs(beta) * c.abs()
+        D = empty(M, N, DT[dtD], pad, off)
+        mcg.gemm_grad_i8("bf16", layoutA, M, N, K, A, ld(A), Q, ld(Q), s.cuda(), C if beta else None, D, ld(D), dtD, beta,
+                         torch.empty(1 << 20, dtype=torch.uint8, device="cuda"))
+        guards_hold(D)
+        within(D, d, grad_tol("bf16", dtD, a, s, d, mag, K), f"{layoutA} {shape} -> {dtD} beta {beta} pad {pad}")
+
+
+# Products on the 256 x 256 and stream-K forms, by sampled rows: first and last, and a
+# few of every tile.
+def sampled(M):
+    return sorted({0, 1, M - 1, M - 2, *range(5, M, 97)})
+
+
+@pytest.mark.parametrize("layoutB", ["k_contig", "mn_contig"])
+@pytest.mark.parametrize("shape", [(4352, 4352, 1024), (4217, 4100, 560), (8192, 1040, 2064)], ids=str)
+def test_large_scaled_products_by_sampled_rows(layoutB, shape):
+    mcg = need_gpu()
+    M, N, K = shape
+    a, b = ref.codes(1, M, K), ref.codes(2, K, N)
+    sa, sb, bias = ref.rand(3, M).abs().float() + 0.1, ref.rand(4, N).abs().float() + 0.1, ref.rand(5, N).float()
+    rows = sampled(M)
+    d = ref.i8_scaled(a[rows], sa[rows], b, sb, bias)
+    core = d - bias.double()
+    for dt, ws in (("bf16", None), ("f32", 64 << 20)):
+        w = None if ws is None else torch.full((ws,), 0x7B, dtype=torch.uint8, device="cuda")
+        D = run_scaled(mcg, a, sa, b, sb, bias, dt, layoutB, ws=w)
+        within(D[rows], d, scaled_tol(d, core, bias, dt), f"{dt} {layoutB} {shape}")
+
+
+@pytest.mark.parametrize("layoutA", ["k_contig", "mn_contig"])
+@pytest.mark.parametrize("shape", [(4352, 4352, 520), (4217, 4100, 1033), (4090, 4090, 1033)], ids=str)
+def test_large_gradient_products_by_sampled_rows(layoutA, shape):
+    mcg = need_gpu()
+    M, N, K = shape
+    a = ref.rand(1, M, K).to(torch.bfloat16)
+    q, s = ref.codes(2, K, N), ref.rand(3, K).abs().float() * 0.02 + 1e-3
+    rows = sampled(M)
+    d, mag = ref.grad_i8(a[rows], q, s, None, 0.0)
+    for dtD, ws in (("bf16", 64 << 20), ("f32", 64 << 20), ("bf16", 14 << 20)):
+        A, Q = put(a if layoutA == "k_contig" else a.T.contiguous()), put(q)
+        D = empty(M, N, DT[dtD])
+        w = torch.full((ws // 4,), float("nan"), device="cuda")
+        mcg.gemm_grad_i8("bf16", layoutA, M, N, K, A, ld(A), Q, ld(Q), s.cuda(), None, D, ld(D), dtD, 0.0, w)
+        torch.cuda.synchronize()
+        assert bool(torch.isfinite(D).all())
+        within(D[rows], d, grad_tol("bf16", dtD, a[rows], s, d, mag, K), f"{dtD} {layoutA} {shape} workspace {ws}")
 
 
 # ------------------------------------------------------------ a layer's step
@@ -508,3 +583,15 @@ def test_a_layers_step_on_another_stream_and_in_a_graph(shape):
         g.replay()
         same(f"replay {rep}")
     say(f"  {shape}: same bits on another stream and in three replays")
+
+
+def test_the_example_learns():
+    need_gpu()
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "linear8_layer.py")
+    spec = importlib.util.spec_from_file_location("linear8_layer", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    losses = example.train(T=300, K=512, N=200, steps=12, rate=0.2)
+    assert all(b < a for a, b in zip(losses, losses[1:])), losses

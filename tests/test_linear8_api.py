@@ -176,6 +176,18 @@ def test_workspace_queries():
     assert m.grad_i8_workspace_bytes("f32", "mn_contig", 256, 256, 8192, FAKE, 256, FAKE, 256, "f32") == 0
 
 
+def test_operands_that_the_gpu_tests_take_in_panels():
+    # (so that tests/test_gpu_linear8.py covers the copies and the widened panels)
+    for M, N, K in ((600, 1300, 2050), (1300, 700, 1999), (1001, 2003, 3001)):
+        for layout, ldb in (("k_contig", K + 7), ("mn_contig", N + 7)):
+            assert m.i8_scaled_workspace_bytes(layout, M, N, K, FAKE, K + 5, FAKE, ldb) >= (M + N) * K
+    for M, N, K in ((512, 1536, 4096), (600, 900, 700), (1001, 1103, 901)):
+        for layout, lda in (("k_contig", K), ("mn_contig", M)):
+            assert m.grad_i8_workspace_bytes("bf16", layout, M, N, K, FAKE, lda, FAKE, N, "bf16") >= 2 * K * N
+    for layout, lda in (("k_contig", 1033), ("mn_contig", 4090)):
+        assert m.grad_i8_workspace_bytes("bf16", layout, 4090, 4090, 1033, FAKE, lda, FAKE, 4090, "f32") >= 4 * 1033 * 4090
+
+
 def test_symbols_have_their_arguments_declared():
     lib = ctypes.CDLL(m.LIB_PATH)
     for fn in ("rmsnorm_quant", "rmsnorm_backward", "quantize_rows", "dequantize_rows", "gemm_i8_scaled",
