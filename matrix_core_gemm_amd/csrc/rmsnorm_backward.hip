@@ -72,13 +72,14 @@ __device__ __forceinline__ void store_dx(const NormGradArgs& p, int64_t row, int
 // One row per TPR threads, NV vectors of eight elements per thread; a workgroup
 // walks the rows a grid apart, the next row's loads in flight while it reduces this
 // one (dX may be dY or dR, so that the compiler itself would keep them behind the
-// stores), and leaves one partial row of dw.  WHOLE: rows of whole vectors.
-template <int DT, int DTX, int TPR, int NV, bool WHOLE>
+// stores), and leaves one partial row of dw.  Rows of at least 8 elements.
+template <int DT, int DTX, int TPR, int NV>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(NormGradArgs p) {
   constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
   constexpr int ES = elem_size<DT>();
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   const int64_t step = (int64_t)gridDim.x * RPW;
+  RowVec at[NV];
   float dw[NV][8];
   Raw8<DT> w[NV], dy[NV], dr[NV];
   Raw8<DTX> xr[NV];
@@ -88,15 +89,15 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(NormGr
     if constexpr (DTX == DT_I8) xs = p.xscale[m];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int64_t c = (int64_t)(v * TPR + t) * 8;
-      dy[v] = load8<DT, WHOLE>(p.dY + m * p.lddy * ES, c, p.N);
-      xr[v] = load8<DTX, WHOLE>(p.X + m * p.ldx * elem_size<DTX>(), c, p.N);
-      if (p.dR) dr[v] = load8<DT, WHOLE>(p.dR + m * p.lddr * ES, c, p.N);
+      dy[v] = load_vec<DT>(p.dY + m * p.lddy * ES, at[v]);
+      xr[v] = load_vec<DTX>(p.X + m * p.ldx * elem_size<DTX>(), at[v]);
+      if (p.dR) dr[v] = load_vec<DT>(p.dR + m * p.lddr * ES, at[v]);
     }
   };
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    if (p.W) w[v] = load8<DT, WHOLE>(p.W, (int64_t)(v * TPR + t) * 8, p.N);
+    at[v] = row_vec((int64_t)(v * TPR + t) * 8, p.N);
+    if (p.W) w[v] = load_vec<DT>(p.W, at[v]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[v][e] = 0.0f;
   }
@@ -119,6 +120,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(NormGr
     if (row + step < p.M) load_row(row + step);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
+      mask_vec(g[v], at[v]);
+      mask_vec(x[v], at[v]);
       float wv[8];
       if (p.W) widen8<DT>(w[v], wv);
 #pragma unroll
@@ -138,7 +141,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(NormGr
         o[e] = rs * __builtin_fmaf(-k, x[v][e], g[v][e]);
         if (p.dR) o[e] += d[v][e];
       }
-      store8<DT, WHOLE>(p.dX + row * p.lddx * ES, (int64_t)(v * TPR + t) * 8, p.N, narrow8<DT>(o));
+      store_vec<DT>(p.dX + row * p.lddx * ES, at[v], narrow8<DT>(o));
     }
   }
   if (!p.dW) return;
@@ -160,10 +163,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(NormGr
   }
   char* part = (char*)(p.part + blockIdx.x * part_stride(p.N));
 #pragma unroll
-  for (int v = 0; v < NV; ++v) store8<DT_F32, WHOLE>(part, (int64_t)(v * TPR + t) * 8, p.N, narrow8<DT_F32>(dw[v]));
+  for (int v = 0; v < NV; ++v) store_vec<DT_F32>(part, at[v], narrow8<DT_F32>(dw[v]));
 }
 
-// Rows of any length: dx with the row read twice, and dw's partial rows column by
+// Rows of any other length: dx with the row read twice, and dw's partial rows column by
 // column (blockIdx.y is the part, threads along the columns).
 template <int DT, int DTX>
 __global__ __launch_bounds__(1024) void norm_grad_long_kernel(NormGradArgs p) {
@@ -252,21 +255,21 @@ __global__ __launch_bounds__(256) void norm_grad_sum_kernel(NormGradArgs p) {
 template <int DT, int DTX, int TPR, int NV>
 static void launch_one(const NormGradArgs& a, hipStream_t s) {
   constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
-  const dim3 grid((unsigned)a.parts), block(RPW * TPR);
-  if (a.N % 8 == 0) hipLaunchKernelGGL((norm_grad_kernel<DT, DTX, TPR, NV, true>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((norm_grad_kernel<DT, DTX, TPR, NV, false>), grid, block, 0, s, a);
+  hipLaunchKernelGGL((norm_grad_kernel<DT, DTX, TPR, NV>), dim3((unsigned)a.parts), dim3(RPW * TPR), 0, s, a);
 }
 
 template <int DT, int DTX>
 static hipError_t launch_dt(const NormGradArgs& a, hipStream_t s) {
   const int64_t n = a.N;
   if (a.M > 0) {
-    if (n <= 512) launch_one<DT, DTX, 64, 1>(a, s);
-    else if (n <= 1024) launch_one<DT, DTX, 64, 2>(a, s);
-    else if (n <= 2048) launch_one<DT, DTX, 256, 1>(a, s);
-    else if (n <= 4096) launch_one<DT, DTX, 256, 2>(a, s);
-    else if (n <= 8192) launch_one<DT, DTX, 512, 2>(a, s);
-    else if (n <= 16384) launch_one<DT, DTX, 1024, 2>(a, s);
+    if (n >= 8 && n <= 512) launch_one<DT, DTX, 64, 1>(a, s);
+    else if (n >= 8 && n <= 1024) launch_one<DT, DTX, 64, 2>(a, s);
+    else if (n >= 8 && n <= 2048) launch_one<DT, DTX, 256, 1>(a, s);
+    else if (n >= 8 && n <= 4096) launch_one<DT, DTX, 256, 2>(a, s);
+    // (as one of 8192, 4999 columns took 89 us instead of 86 for 8000 rows)
+    else if (n >= 8 && n <= 6144) launch_one<DT, DTX, 384, 2>(a, s);
+    else if (n >= 8 && n <= 8192) launch_one<DT, DTX, 512, 2>(a, s);
+    else if (n >= 8 && n <= 16384) launch_one<DT, DTX, 1024, 2>(a, s);
     else {
       if (a.dW) {  // first: dX may be the memory of dY
         const dim3 grid((unsigned)((n + 2047) / 2048), (unsigned)a.parts);

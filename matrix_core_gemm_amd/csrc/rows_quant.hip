@@ -124,12 +124,12 @@ __device__ __forceinline__ void top8(const float (&y)[8], uint32_t& top) {
 }
 
 // TPR threads per row (a wavefront or a workgroup), NV vectors of eight elements
-// per thread: rows of up to 8 * TPR * NV elements (WHOLE: of whole vectors).  A workgroup walks rows a grid
+// per thread: rows of 8 to 8 * TPR * NV elements.  A workgroup walks rows a grid
 // apart: the weights stay in its registers, and the next row's loads go out before
 // this row's stores (which the compiler would otherwise keep them behind, since H
 // may be X).  With the loads of every row behind the previous stores, 8192 x 8192
 // bf16 with a residual took 270 us.
-template <int DT, bool NORM, int TPR, int NV, bool WHOLE>
+template <int DT, bool NORM, int TPR, int NV>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rows_quant_kernel(RowsQuantArgs p) {
   constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
   constexpr int ES = elem_size<DT>();
@@ -137,20 +137,22 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rows_quant_kernel(RowsQ
   const int64_t step = (int64_t)gridDim.x * RPW;
   int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / TPR;
   if (row >= p.M) return;  // whole wavefronts, and only where a row is one wavefront
+  RowVec at[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) at[v] = row_vec((int64_t)(v * TPR + t) * 8, p.N);
   Raw8<DT> x[NV], r[NORM ? NV : 1], w[NORM ? NV : 1];
   auto load_row = [&](int64_t m) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int64_t c = (int64_t)(v * TPR + t) * 8;
-      x[v] = load8<DT, WHOLE>(p.X + m * p.ldx * ES, c, p.N);
+      x[v] = load_vec<DT>(p.X + m * p.ldx * ES, at[v]);
       if constexpr (NORM)
-        if (p.R) r[v] = load8<DT, WHOLE>(p.R + m * p.ldr * ES, c, p.N);
+        if (p.R) r[v] = load_vec<DT>(p.R + m * p.ldr * ES, at[v]);
     }
   };
   if constexpr (NORM) {
     if (p.W) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v) w[v] = load8<DT, WHOLE>(p.W, (int64_t)(v * TPR + t) * 8, p.N);
+      for (int v = 0; v < NV; ++v) w[v] = load_vec<DT>(p.W, at[v]);
     }
   }
   load_row(row);
@@ -174,8 +176,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rows_quant_kernel(RowsQ
     uint32_t top = 0;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
+      mask_vec(y[v], at[v]);
       if constexpr (NORM) {
-        if (p.H) store8<DT, WHOLE>(p.H + row * p.ldh * ES, (int64_t)(v * TPR + t) * 8, p.N, narrow8<DT>(y[v]));
+        if (p.H) store_vec<DT>(p.H + row * p.ldh * ES, at[v], narrow8<DT>(y[v]));
         stat8(y[v], ss);
         if (p.W) {
           float z[8];
@@ -189,8 +192,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rows_quant_kernel(RowsQ
     row_reduce<TPR>(ss, top, phase);
     const RowStat s = row_stat<NORM>(ss, top, p.N, p.eps);
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
-      store8<DT_I8, WHOLE>((char*)p.Q + row * p.ldq, (int64_t)(v * TPR + t) * 8, p.N, codes8(y[v], s));
+    for (int v = 0; v < NV; ++v) store_vec<DT_I8>((char*)p.Q + row * p.ldq, at[v], codes8(y[v], s));
     if (t == 0) {
       p.scale[row] = s.scale;
       if (NORM && p.rstd) p.rstd[row] = s.rstd;
@@ -198,8 +200,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rows_quant_kernel(RowsQ
   }
 }
 
-// Rows of any length: the row is read a second time (through the caches) for its
-// codes.  H is written in the second pass, by the thread that has just read the
+// Rows of any other length: the row is read a second time (through the caches) for
+// its codes.  H is written in the second pass, by the thread that has just read the
 // same elements of X and R, so it may be either of them.
 template <int DT, bool NORM>
 __global__ __launch_bounds__(1024) void rows_quant_long_kernel(RowsQuantArgs p) {
@@ -237,12 +239,15 @@ __global__ __launch_bounds__(1024) void rows_quant_long_kernel(RowsQuantArgs p) 
   }
 }
 
-// The values of 8-bit rows: one vector of eight codes per thread, columns along x.
+// The values of 8-bit rows: one vector of eight codes per thread, columns along x;
+// short rows share a workgroup, `rows` of `vecs` vectors (8000 x 300: 6.2 us with a
+// workgroup each, 3.9 so).
 template <int DT>
-__global__ __launch_bounds__(256) void rows_dequant_kernel(RowsDequantArgs p) {
-  const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-  if (c >= p.N) return;
-  for (int64_t row = blockIdx.y; row < p.M; row += gridDim.y) {
+__global__ __launch_bounds__(256) void rows_dequant_kernel(RowsDequantArgs p, int vecs, int rows) {
+  const int sub = threadIdx.x / vecs;
+  const int64_t c = ((int64_t)blockIdx.x * 256 + threadIdx.x % vecs) * 8;
+  if (c >= p.N || sub >= rows) return;
+  for (int64_t row = (int64_t)blockIdx.y * rows + sub; row < p.M; row += (int64_t)gridDim.y * rows) {
     float x[8];
     widen8<DT_I8>(load8<DT_I8>((const char*)p.Q + row * p.ldq, c, p.N), x);
     const float s = p.scale[row];
@@ -256,21 +261,23 @@ template <int DT, bool NORM, int TPR, int NV>
 static hipError_t launch_one(const RowsQuantArgs& a, int num_cu, hipStream_t s) {
   constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
   const int64_t blocks = min((a.M + RPW - 1) / RPW, (int64_t)num_cu * WG_PER_CU);
-  const dim3 grid((unsigned)blocks), block(RPW * TPR);
-  if (a.N % 8 == 0) hipLaunchKernelGGL((rows_quant_kernel<DT, NORM, TPR, NV, true>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((rows_quant_kernel<DT, NORM, TPR, NV, false>), grid, block, 0, s, a);
+  hipLaunchKernelGGL((rows_quant_kernel<DT, NORM, TPR, NV>), dim3((unsigned)blocks), dim3(RPW * TPR), 0, s, a);
   return hipGetLastError();
 }
 
 template <int DT, bool NORM>
 static hipError_t launch_dt(const RowsQuantArgs& a, int num_cu, hipStream_t s) {
   const int64_t n = a.N;
-  if (n <= 512) return launch_one<DT, NORM, 64, 1>(a, num_cu, s);
-  if (n <= 1024) return launch_one<DT, NORM, 64, 2>(a, num_cu, s);
-  if (n <= 2048) return launch_one<DT, NORM, 256, 1>(a, num_cu, s);
-  if (n <= 4096) return launch_one<DT, NORM, 256, 2>(a, num_cu, s);
-  if (n <= 8192) return a.M <= num_cu ? launch_one<DT, NORM, 1024, 1>(a, num_cu, s) : launch_one<DT, NORM, 256, 4>(a, num_cu, s);
-  if (n <= 16384) return launch_one<DT, NORM, 1024, 2>(a, num_cu, s);
+  if (n >= 8) {
+    if (n <= 512) return launch_one<DT, NORM, 64, 1>(a, num_cu, s);
+    if (n <= 1024) return launch_one<DT, NORM, 64, 2>(a, num_cu, s);
+    if (n <= 2048) return launch_one<DT, NORM, 256, 1>(a, num_cu, s);
+    if (n <= 4096) return launch_one<DT, NORM, 256, 2>(a, num_cu, s);
+    // (as one of 8192, 5000 columns took 55 us instead of 48 for 8000 rows)
+    if (n <= 6144 && a.M > num_cu) return launch_one<DT, NORM, 256, 3>(a, num_cu, s);
+    if (n <= 8192) return a.M <= num_cu ? launch_one<DT, NORM, 1024, 1>(a, num_cu, s) : launch_one<DT, NORM, 256, 4>(a, num_cu, s);
+    if (n <= 16384) return launch_one<DT, NORM, 1024, 2>(a, num_cu, s);
+  }
   hipLaunchKernelGGL((rows_quant_long_kernel<DT, NORM>), dim3((unsigned)min(a.M, MAX_BLOCKS)), dim3(1024), 0, s, a);
   return hipGetLastError();
 }
@@ -289,10 +296,12 @@ hipError_t launch_rows_quant(int dt, bool norm, const RowsQuantArgs& a, int num_
 }
 
 hipError_t launch_rows_dequant(int dt, const RowsDequantArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.N + 2047) / 2048), (unsigned)(a.M < 65535 ? a.M : 65535));
-  if (dt == DT_BF16) hipLaunchKernelGGL((rows::rows_dequant_kernel<DT_BF16>), grid, dim3(256), 0, s, a);
-  else if (dt == DT_F16) hipLaunchKernelGGL((rows::rows_dequant_kernel<DT_F16>), grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((rows::rows_dequant_kernel<rows::DT_F32>), grid, dim3(256), 0, s, a);
+  const int vecs = a.N < 2048 ? (int)((a.N + 7) / 8) : 256, rows = 256 / vecs;
+  const int64_t groups = (a.M + rows - 1) / rows;
+  const dim3 grid((unsigned)((a.N + 2047) / 2048), (unsigned)(groups < 65535 ? groups : 65535));
+  if (dt == DT_BF16) hipLaunchKernelGGL((rows::rows_dequant_kernel<DT_BF16>), grid, dim3(256), 0, s, a, vecs, rows);
+  else if (dt == DT_F16) hipLaunchKernelGGL((rows::rows_dequant_kernel<DT_F16>), grid, dim3(256), 0, s, a, vecs, rows);
+  else hipLaunchKernelGGL((rows::rows_dequant_kernel<rows::DT_F32>), grid, dim3(256), 0, s, a, vecs, rows);
   return hipGetLastError();
 }
 
