@@ -54,6 +54,8 @@ if not os.path.exists(LIB_PATH):
                       "(or __graft_entry__.build()); there is no non-GPU fallback")
 
 _lib = ctypes.CDLL(LIB_PATH)
+from . import _mcgcall  # noqa: E402  (calls into the same library)
+
 _i32, _i64, _dbl, _f32, _vp = ctypes.c_int, ctypes.c_int64, ctypes.c_double, ctypes.c_float, ctypes.c_void_p
 _lib.gemm_dense.argtypes = [_i32, _i32, _i32, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64,
                             _vp, _vp, _i64, _i32, _dbl, _dbl, _f32, _f32, _vp]
@@ -160,6 +162,9 @@ def _stream(stream):
 def _check(fn: str, status: int) -> None:
     if status != 0:
         raise MCGError(fn, status)
+
+
+_mcgcall.setup(DTYPES, LAYOUTS, _stream, _raw_stream, _raw_device)
 
 
 def gemm_dense(dtypeA, dtypeB, layoutA, layoutB, M, N, K, A, lda, B, ldb, C, D, ldc, dtypeD,
@@ -334,19 +339,19 @@ def _workspace(workspace, workspace_bytes):
 def rmsnorm_quant(dtype, M, N, X, ldx, R, ldr, weight, eps, H, ldh, Q, ldq, scale, rstd=None, stream=None) -> None:
     """Root-mean-square norm of X + R in 8 bits: codes Q with a scale per row; H
     receives the sum and rstd the norms' factors (each may be None)."""
-    _check("rmsnorm_quant", _lib.rmsnorm_quant(
-        _dt(dtype), M, N, _ptr(X), ldx, _ptr(R), ldr, _ptr(weight), float(eps), _ptr(H), ldh, _ptr(Q), ldq,
-        _ptr(scale), _ptr(rstd), _stream(stream)))
+    status = _mcgcall.rmsnorm_quant(dtype, M, N, X, ldx, R, ldr, weight, eps, H, ldh, Q, ldq, scale, rstd, stream)
+    if status:
+        raise MCGError("rmsnorm_quant", status)
 
 
 def rmsnorm_backward(dtype, dtypeX, M, N, dY, lddy, X, ldx, scaleX, weight, rstd, dR, lddr, dX, lddx, dW,
                      workspace=None, workspace_bytes=0, stream=None) -> None:
     """Gradient of the norm: dX (with dR added) and dW, from X in dtype or as 8-bit
     codes with scaleX.  dW needs rmsnorm_backward_workspace_bytes(M, N) of workspace."""
-    ws, nb = _workspace(workspace, workspace_bytes)
-    _check("rmsnorm_backward", _lib.rmsnorm_backward(
-        _dt(dtype), _dt(dtypeX), M, N, _ptr(dY), lddy, _ptr(X), ldx, _ptr(scaleX), _ptr(weight), _ptr(rstd),
-        _ptr(dR), lddr, _ptr(dX), lddx, _ptr(dW), ws, nb, _stream(stream)))
+    status = _mcgcall.rmsnorm_backward(dtype, dtypeX, M, N, dY, lddy, X, ldx, scaleX, weight, rstd, dR, lddr, dX, lddx,
+                                       dW, workspace, workspace_bytes, stream)
+    if status:
+        raise MCGError("rmsnorm_backward", status)
 
 
 def rmsnorm_backward_workspace_bytes(M, N) -> int:
@@ -356,24 +361,27 @@ def rmsnorm_backward_workspace_bytes(M, N) -> int:
 
 def quantize_rows(dtype, M, N, X, ldx, Q, ldq, scale, stream=None) -> None:
     """The rows of X as 8-bit codes with a scale each."""
-    _check("quantize_rows", _lib.quantize_rows(_dt(dtype), M, N, _ptr(X), ldx, _ptr(Q), ldq, _ptr(scale),
-                                               _stream(stream)))
+    status = _mcgcall.quantize_rows(dtype, M, N, X, ldx, Q, ldq, scale, stream)
+    if status:
+        raise MCGError("quantize_rows", status)
 
 
 def dequantize_rows(dtypeD, M, N, Q, ldq, scale, D, ldd, stream=None) -> None:
     """The values of 8-bit rows, rounded once to dtypeD."""
-    _check("dequantize_rows", _lib.dequantize_rows(_dt(dtypeD), M, N, _ptr(Q), ldq, _ptr(scale), _ptr(D), ldd,
-                                                   _stream(stream)))
+    status = _mcgcall.dequantize_rows(dtypeD, M, N, Q, ldq, scale, D, ldd, stream)
+    if status:
+        raise MCGError("dequantize_rows", status)
 
 
 def gemm_i8_scaled(layoutB, M, N, K, A, lda, scaleA, B, ldb, scaleB, bias, D, ldd, dtypeD, workspace=None,
                    workspace_bytes=0, stream=None) -> None:
-    """D = scaleA[i] * scaleB[j] * (A . B) + bias[j] on int8 operands; a workspace
-    (up to i8_scaled_workspace_bytes) lets few-tile products cut K."""
-    ws, nb = _workspace(workspace, workspace_bytes)
-    _check("gemm_i8_scaled", _lib.gemm_i8_scaled(
-        _lay(layoutB), M, N, K, _ptr(A), lda, _ptr(scaleA), _ptr(B), ldb, _ptr(scaleB), _ptr(bias), _ptr(D), ldd,
-        _dt(dtypeD), ws, nb, _stream(stream)))
+    """D = scaleA[i] * scaleB[j] * (A . B) + bias[j] on int8 operands; a workspace (up
+    to i8_scaled_workspace_bytes) lets few-tile products cut K, and operands without
+    16-byte rows take the faster kernels."""
+    status = _mcgcall.gemm_i8_scaled(layoutB, M, N, K, A, lda, scaleA, B, ldb, scaleB, bias, D, ldd, dtypeD, workspace,
+                                     workspace_bytes, stream)
+    if status:
+        raise MCGError("gemm_i8_scaled", status)
 
 
 def i8_scaled_workspace_bytes(layoutB, M, N, K, A, lda, B, ldb) -> int:
@@ -384,11 +392,12 @@ def i8_scaled_workspace_bytes(layoutB, M, N, K, A, lda, B, ldb) -> int:
 def gemm_grad_i8(dtypeA, layoutA, M, N, K, A, lda, Q, ldq, scaleK, C, D, ldd, dtypeD, beta=0.0, workspace=None,
                  workspace_bytes=0, stream=None) -> None:
     """D = A . (scaleK[k] * Q[k]) + beta * C, A 16-bit and Q int8 rows: the weight
-    gradient from an 8-bit checkpoint, or the input gradient from 8-bit weights."""
-    ws, nb = _workspace(workspace, workspace_bytes)
-    _check("gemm_grad_i8", _lib.gemm_grad_i8(
-        _dt(dtypeA), _lay(layoutA), M, N, K, _ptr(A), lda, _ptr(Q), ldq, _ptr(scaleK), _ptr(C), _ptr(D), ldd,
-        _dt(dtypeD), float(beta), ws, nb, _stream(stream)))
+    gradient from an 8-bit checkpoint, or the input gradient from 8-bit weights.  A
+    workspace (up to grad_i8_workspace_bytes) is what the faster forms work in."""
+    status = _mcgcall.gemm_grad_i8(dtypeA, layoutA, M, N, K, A, lda, Q, ldq, scaleK, C, D, ldd, dtypeD, beta, workspace,
+                                   workspace_bytes, stream)
+    if status:
+        raise MCGError("gemm_grad_i8", status)
 
 
 def grad_i8_workspace_bytes(dtypeA, layoutA, M, N, K, A, lda, Q, ldq, dtypeD) -> int:

@@ -2,18 +2,22 @@
 
 Every source is compiled by hipcc for gfx950 only; objects go to
 matrix_core_gemm_amd/_build/ and are linked into one shared library that the
-Python binding loads with ctypes.
+Python binding loads with ctypes.  _mcgcall.so (csrc/pycall.c, plain C) calls the
+small operators in it without ctypes.
 """
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "_libmcg.so")
+CALL = os.path.join(HERE, "_mcgcall.so")
+CC = os.environ.get("CC", "gcc")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["gemm_dense.hip", "gemm_skinny_n.hip", "gemm_skinny_m.hip", "gemm_stream.hip", "gemm_fast.hip", "gemm_fast_mid.hip", "gemm_fast_sk.hip", "gemm_fast_mid_sk.hip", "gemm_sparse.hip",
@@ -77,7 +81,17 @@ def build(force: bool = True, verbose: bool = False) -> str:
     tmp = LIB + ".tmp"
     subprocess.check_call([HIPCC, "-shared", "-fPIC", "--offload-arch=gfx950", *objs, "-o", tmp])
     os.replace(tmp, LIB)
+    build_call()
     return LIB
+
+
+def build_call() -> str:
+    tmp = CALL + ".tmp"
+    subprocess.check_call([CC, "-O2", "-std=gnu11", "-Wall", "-shared", "-fPIC", "-I" + sysconfig.get_paths()["include"],
+                           os.path.join(CSRC, "pycall.c"), "-o", tmp, "-L" + HERE, "-l:" + os.path.basename(LIB),
+                           "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, CALL)
+    return CALL
 
 
 if __name__ == "__main__":

@@ -188,6 +188,22 @@ def test_operands_that_the_gpu_tests_take_in_panels():
         assert m.grad_i8_workspace_bytes("bf16", layout, 4090, 4090, 1033, FAKE, lda, FAKE, 4090, "f32") >= 4 * 1033 * 4090
 
 
+def test_arguments_that_are_none_of_the_accepted_kinds():
+    kw = rmsnorm_quant_args(stream=0)
+    for bad, error in (({"X": "x"}, AttributeError), ({"M": 1.5}, TypeError), ({"dtype": "f17"}, KeyError), ({"eps": "1"}, TypeError),
+                       ({"M": 1 << 70}, OverflowError), ({"stream": "s"}, (TypeError, ValueError)), ({"M": "1", "X": "x"}, TypeError)):
+        with pytest.raises(error):
+            m.rmsnorm_quant(**{**kw, **bad})
+    with pytest.raises(TypeError):
+        m.quantize_rows("bf16", 1, 8, FAKE)
+
+
+def test_one_copy_of_the_library_is_loaded():
+    with open("/proc/self/maps") as f:
+        files = {line.split()[-1] for line in f if "_libmcg.so" in line}
+    assert files == {m.LIB_PATH}
+
+
 def test_symbols_have_their_arguments_declared():
     lib = ctypes.CDLL(m.LIB_PATH)
     for fn in ("rmsnorm_quant", "rmsnorm_backward", "quantize_rows", "dequantize_rows", "gemm_i8_scaled",
