@@ -442,7 +442,8 @@ void gemm_fast_kernel(typename KernelTypes<Op>::Args p) {
     }
     return o;
   };
-  bool by_rows = vec_ok && em0 + BM <= d.M && en0 + BN <= d.N;
+  const bool interior = vec_ok && em0 + BM <= d.M && en0 + BN <= d.N;
+  bool by_rows = interior;
   if constexpr (SCALED) by_rows = by_rows || d.sa;  // (checks the bounds itself)
   if (by_rows) {
     // Interior tile.  Each wavefront passes the 32 x 64 block of its row group i
@@ -506,9 +507,19 @@ void gemm_fast_kernel(typename KernelTypes<Op>::Args p) {
           for (int t = 0; t < 8; ++t) sa[t] = d.sa[min(row0 + 4 * t, d.M - 1)];
           v4 a[8];
           through_lds(i, wbuf + (KS ? 0 : (i & 1) * 8192), a, [] {});
+          if (interior) {
 #pragma unroll
-          for (int t = 0; t < 8; ++t)
-            if (row0 + 4 * t < d.M && col < d.N) scaled_store4(p, row0 + 4 * t, col, a[t], sa[t], cols);
+            for (int t = 0; t < 8; ++t) {
+              float o[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[e] = scaled_value(a[t][e], sa[t], cols.sb[e], cols.bias[e]);
+              scaled_put4(d.D, (row0 + 4 * t) * d.ld + col, out, o, true, 4);
+            }
+          } else {
+#pragma unroll
+            for (int t = 0; t < 8; ++t)
+              if (row0 + 4 * t < d.M && col < d.N) scaled_store4(p, row0 + 4 * t, col, a[t], sa[t], cols);
+          }
         }
         return;
       }

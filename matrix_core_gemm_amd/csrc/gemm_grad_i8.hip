@@ -102,7 +102,7 @@ __global__ __launch_bounds__(256, TWO && BM == 128 ? 1 : 2) void grad_general_ke
   const int kt0 = (int)blockIdx.y * p.kt_per_split;
   const int nk = min(nk_all - kt0, p.kt_per_split);
 
-  // Two K tiles ahead in registers, two stages in LDS (see gemm_i8_scaled.hip).
+  // SETS K tiles ahead in registers, two stages in LDS (see gemm_i8_scaled.hip).
   using LdA = AnyLoader<2, LA, BM, NT>;
   using LdQ = AnyLoader<1, LAYOUT_MN, BN, NT, KE>;
   constexpr int QPT = LdQ::PER_THREAD;
@@ -110,9 +110,10 @@ __global__ __launch_bounds__(256, TWO && BM == 128 ? 1 : 2) void grad_general_ke
   LdQ lq;
   la.init(p.A, p.lda, m0, p.M, p.K, tid);
   lq.init(p.Q, p.ldq, n0, p.N, p.K, tid);
-  typename LdA::Regs ra[2];
-  typename LdQ::Regs q[2];
-  float sk[2][QPT];
+  constexpr int SETS = 2;
+  typename LdA::Regs ra[SETS];
+  typename LdQ::Regs q[SETS];
+  float sk[SETS][QPT];
   auto load_tile = [&](auto set_c, int kt) {
     constexpr int set = decltype(set_c)::value;
     la.load(ra[set], kt0 + kt, kt < nk);
@@ -124,7 +125,7 @@ __global__ __launch_bounds__(256, TWO && BM == 128 ? 1 : 2) void grad_general_ke
   };
   auto store_tile = [&](auto set_c, int kt) {
     constexpr int set = decltype(set_c)::value;
-    lds_char* st = smem + set * STAGE;
+    lds_char* st = smem + (set & 1) * STAGE;
     la.settle(ra[set], kt0 + kt);
     lq.settle(q[set], kt0 + kt);
     la.store(ra[set], st);
@@ -147,11 +148,11 @@ __global__ __launch_bounds__(256, TWO && BM == 128 ? 1 : 2) void grad_general_ke
   for (int i = 0; i < WTM; ++i)
 #pragma unroll
     for (int j = 0; j < WTN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  auto step = [&](auto cur_c, int kt) {
-    constexpr int set = decltype(cur_c)::value;
-    lds_char* cur = smem + set * STAGE;
-    store_tile(std::integral_constant<int, set ^ 1>{}, kt + 1);
-    load_tile(std::integral_constant<int, set ^ 1>{}, kt + 3);
+  auto step = [&](auto set_c, int kt) {
+    constexpr int set = decltype(set_c)::value;
+    lds_char* cur = smem + (set & 1) * STAGE;
+    store_tile(std::integral_constant<int, (set + 1) % SETS>{}, kt + 1);
+    load_tile(std::integral_constant<int, (set + 1) % SETS>{}, kt + 1 + SETS);
 #pragma unroll
     for (int st = 0; st < Op::STEPS; ++st) {
       i32x4 fa[WTM], fb[WTN];
@@ -169,19 +170,11 @@ __global__ __launch_bounds__(256, TWO && BM == 128 ? 1 : 2) void grad_general_ke
     }
     barrier_tiles();
   };
-  constexpr std::integral_constant<int, 0> even;
-  constexpr std::integral_constant<int, 1> odd;
-  load_tile(even, 0);
-  load_tile(odd, 1);
-  store_tile(even, 0);
-  load_tile(even, 2);
+  for_each_set<SETS>([&](auto set) { load_tile(set, set); });
+  store_tile(std::integral_constant<int, 0>{}, 0);
+  load_tile(std::integral_constant<int, 0>{}, SETS);
   barrier_tiles();
-  int kt = 0;
-  for (; kt + 2 <= nk; kt += 2) {
-    step(even, kt);
-    step(odd, kt + 1);
-  }
-  if (kt < nk) step(even, kt);
+  for (int kt = 0; kt < nk; kt += SETS) for_each_set<SETS>([&](auto set) { step(set, kt + set); });
   static_assert(BM * 512 <= 2 * STAGE, "epilogue stage");
   store_tile_rows<WG, BM>(smem, acc, tid, [&](int r, int c, const f32x4& v) {
     const int64_t m = m0 + r, n = n0 + c;

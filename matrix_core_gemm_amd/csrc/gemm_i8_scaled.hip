@@ -39,7 +39,7 @@ __global__ __launch_bounds__(256, 2) void scaled_general_kernel(ScaledArgs p) {
   const int kt0 = (int)blockIdx.y * p.kt_per_split;
   const int nk = min(nk_all - kt0, p.kt_per_split);
 
-  // Two K tiles ahead in registers, two stages in LDS.  (One tile ahead, with loads the
+  // SETS K tiles ahead in registers, two stages in LDS.  (One tile ahead, with loads the
   // compiler waited for at the end of every condition around them: one token x 8000 x
   // 8000, rows 8003 apart, 29 us; so 17.4, the streaming kernel's time for aligned rows.)
   using LdA = AnyLoader<1, LAYOUT_K, BM, NT>;
@@ -48,8 +48,9 @@ __global__ __launch_bounds__(256, 2) void scaled_general_kernel(ScaledArgs p) {
   LdB lb;
   la.init(p.A, p.lda, m0, p.M, p.K, tid);
   lb.init(p.B, p.ldb, n0, p.N, p.K, tid);
-  typename LdA::Regs ra[2];
-  typename LdB::Regs rb[2];
+  constexpr int SETS = 2;
+  typename LdA::Regs ra[SETS];
+  typename LdB::Regs rb[SETS];
   auto load_tile = [&](auto set_c, int kt) {
     constexpr int set = decltype(set_c)::value;
     la.load(ra[set], kt0 + kt, kt < nk);
@@ -59,19 +60,20 @@ __global__ __launch_bounds__(256, 2) void scaled_general_kernel(ScaledArgs p) {
     constexpr int set = decltype(set_c)::value;
     la.settle(ra[set], kt0 + kt);
     lb.settle(rb[set], kt0 + kt);
-    la.store(ra[set], ldsA[set]);
-    lb.store(rb[set], ldsB[set]);
+    la.store(ra[set], ldsA[set & 1]);
+    lb.store(rb[set], ldsB[set & 1]);
   };
   i32x4 acc[WTM][WTN];
 #pragma unroll
   for (int i = 0; i < WTM; ++i)
 #pragma unroll
     for (int j = 0; j < WTN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-  // K tile kt in stage cur = kt % 2; tile kt + 1 goes from its registers to the other stage
-  auto step = [&](auto cur_c, int kt) {
-    constexpr int cur = decltype(cur_c)::value;
-    store_tile(std::integral_constant<int, cur ^ 1>{}, kt + 1);
-    load_tile(std::integral_constant<int, cur ^ 1>{}, kt + 3);
+  // K tile kt, in stage kt % 2; tile kt + 1 goes from its registers to the other stage.
+  // Tiles past the range are zeros, so that the last steps need no conditions.
+  auto step = [&](auto set_c, int kt) {
+    constexpr int set = decltype(set_c)::value, cur = set & 1;
+    store_tile(std::integral_constant<int, (set + 1) % SETS>{}, kt + 1);
+    load_tile(std::integral_constant<int, (set + 1) % SETS>{}, kt + 1 + SETS);
 #pragma unroll
     for (int s = 0; s < Op::STEPS; ++s) {
       i32x4 fa[WTM], fb[WTN];
@@ -86,19 +88,11 @@ __global__ __launch_bounds__(256, 2) void scaled_general_kernel(ScaledArgs p) {
     }
     barrier_tiles();
   };
-  constexpr std::integral_constant<int, 0> even;
-  constexpr std::integral_constant<int, 1> odd;
-  load_tile(even, 0);
-  load_tile(odd, 1);
-  store_tile(even, 0);
-  load_tile(even, 2);
+  for_each_set<SETS>([&](auto set) { load_tile(set, set); });
+  store_tile(std::integral_constant<int, 0>{}, 0);
+  load_tile(std::integral_constant<int, 0>{}, SETS);
   barrier_tiles();
-  int kt = 0;
-  for (; kt + 2 <= nk; kt += 2) {
-    step(even, kt);
-    step(odd, kt + 1);
-  }
-  if (kt < nk) step(even, kt);
+  for (int kt = 0; kt < nk; kt += SETS) for_each_set<SETS>([&](auto set) { step(set, kt + set); });
   static_assert(BM * 512 <= 2 * (GA::BYTES + GB::BYTES), "epilogue stage");
   if (p.splits > 1) {
     store_tile_rows<WG, BM>(smem, acc, tid, [&](int r, int c, const i32x4& v) {
@@ -144,7 +138,7 @@ namespace {
 TileCost general_cost(int rows) {
   return rows == 32   ? TileCost{0.65, 0.65, 4, 3.0}
          : rows == 64 ? TileCost{0.85, 0.7, 3, 4.0}
-                      : TileCost{1.2, 0.8, 2, 5.0};
+                      : TileCost{1.2, 0.8, 2, 9.0};
 }
 int64_t cdiv(int64_t x, int64_t y) { return (x + y - 1) / y; }
 int64_t round_up(int64_t x, int64_t y) { return cdiv(x, y) * y; }

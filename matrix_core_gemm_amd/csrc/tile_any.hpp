@@ -146,6 +146,15 @@ struct AnyLoader {
 inline bool any_operand_ok(int64_t eb, int64_t rows, int64_t cols, int64_t ld) {
   return rows > 0 && cols > 0 && ((rows - 1) * ld + cols) * eb >= 16;
 }
+// f(0), f(1), ... as compile-time constants: register sets of successive K tiles.
+template <int N, class F, int I = 0>
+__device__ __forceinline__ void for_each_set(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    for_each_set<N, F, I + 1>(static_cast<F&&>(f));
+  }
+}
+
 // Rows of the general kernels' tiles: the fewest that hold M, up to 128 (32 x 4096 x
 // 4096 from 8-bit weights 15.9 us with 32 rows, 25 with 128; 64 rows 21.4 and 25; a
 // second row of tiles would read B twice).
