@@ -253,7 +253,7 @@ TileCost general_cost(int rows, bool two) {
   if (two)
     return rows == 32   ? TileCost{1.0, 0.65, 2, 3.0}
            : rows == 64 ? TileCost{1.2, 0.8, 2, 4.0}
-                        : TileCost{1.5, 1.5, 1, 8.0};
+                        : TileCost{1.6, 1.6, 1, 8.0};
   return rows == 32   ? TileCost{0.75, 0.5, 4, 3.0}
          : rows == 64 ? TileCost{0.85, 0.6, 3, 4.0}
                       : TileCost{1.1, 0.78, 2, 8.0};

@@ -98,6 +98,7 @@ struct StreamArgs {
   using type = DenseArgs;
   template <int BW>
   static constexpr int steps() { return 1; }
+  static constexpr bool SHORT = false;
 };
 template <>
 struct StreamArgs<I8Scaled> {
@@ -108,6 +109,9 @@ struct StreamArgs<I8Scaled> {
   // 24 x 4096 x 16384 28.3 and 26.7 (18.7 with K in two ranges)
   template <int BW>
   static constexpr int steps() { return BW == 32 ? 3 : BW == 64 ? 2 : 1; }
+  // ranges that fit the ring have a loop of their own (9 x 64 x 128: 5.7 us through
+  // 15 stages, most of them zeros, 4.9 so)
+  static constexpr bool SHORT = true;
 };
 
 template <class Op, int LA, int LB, bool WIDE_A, int BW>
@@ -181,35 +185,43 @@ __global__ __launch_bounds__(THREADS) void gemm_stream_kernel(typename StreamArg
   };
 
   acc_t acc{};
+  auto multiply = [&](int t) {
+    const lds_char* sA = stage(t);
+    const lds_char* sB = sA + GA::BYTES;
+    // instruction s of the stage goes to K group (t * SPS + s) mod KG
 #pragma unroll
-  for (int t = 0; t < NS - U; ++t) issue(t);
-  for (int t0 = 0; t0 < nkl; t0 += U) {
-    wait_vmcnt<(NS - 2 * U) * IPS>();  // this wave's part of tiles t0 .. t0 + U - 1 has landed
-    barrier_lds();                     // ... and every wave's; the stages of the U tiles before are free
-#pragma unroll
-    for (int u = 0; u < U; ++u) issue(t0 + NS - U + u);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {  // (tiles past the range are zeros)
-      const int t = t0 + u;
-      const lds_char* sA = stage(t);
-      const lds_char* sB = sA + GA::BYTES;
-      // instruction s of the stage goes to K group (t * SPS + s) mod KG
-#pragma unroll
-      for (int s = 0; s < SPS; ++s) {
-        if (KG > 1 && (t * SPS + s) % KG != kg) continue;
-        const int kb = 2 * LB16 * s + LB16 * g;  // lane group g's K bytes of instruction s
-        // a K-contiguous operand's ordinary reads go before the other's asm block,
-        // whose wait then covers them
-        frag_t fa, fb;
-        if constexpr (LA == LAYOUT_K || LB == LAYOUT_MN) {
-          fa = StreamFrag<Op, RdA, LA, RA_ROWS * EB>::read(sA, rbA, kb, lane);
-          fb = StreamFrag<Op, RdB, LB, RB_ROWS * EB>::read(sB, rbB, kb, lane);
-        } else {
-          fb = StreamFrag<Op, RdB, LB, RB_ROWS * EB>::read(sB, rbB, kb, lane);
-          fa = StreamFrag<Op, RdA, LA, RA_ROWS * EB>::read(sA, rbA, kb, lane);
-        }
-        Op::mma(acc, fb, fa);
+    for (int s = 0; s < SPS; ++s) {
+      if (KG > 1 && (t * SPS + s) % KG != kg) continue;
+      const int kb = 2 * LB16 * s + LB16 * g;  // lane group g's K bytes of instruction s
+      // a K-contiguous operand's ordinary reads go before the other's asm block,
+      // whose wait then covers them
+      frag_t fa, fb;
+      if constexpr (LA == LAYOUT_K || LB == LAYOUT_MN) {
+        fa = StreamFrag<Op, RdA, LA, RA_ROWS * EB>::read(sA, rbA, kb, lane);
+        fb = StreamFrag<Op, RdB, LB, RB_ROWS * EB>::read(sB, rbB, kb, lane);
+      } else {
+        fb = StreamFrag<Op, RdB, LB, RB_ROWS * EB>::read(sB, rbB, kb, lane);
+        fa = StreamFrag<Op, RdA, LA, RA_ROWS * EB>::read(sA, rbA, kb, lane);
       }
+      Op::mma(acc, fb, fa);
+    }
+  };
+  if (StreamArgs<Op>::SHORT && nkl <= NS - U) {
+    // a range that fits the ring: no stages of zeros, one wait
+    for (int t = 0; t < nkl; ++t) issue(t);
+    wait_vmcnt<0>();
+    barrier_lds();
+    for (int t = 0; t < nkl; ++t) multiply(t);
+  } else {
+#pragma unroll
+    for (int t = 0; t < NS - U; ++t) issue(t);
+    for (int t0 = 0; t0 < nkl; t0 += U) {
+      wait_vmcnt<(NS - 2 * U) * IPS>();  // this wave's part of tiles t0 .. t0 + U - 1 has landed
+      barrier_lds();                     // ... and every wave's; the stages of the U tiles before are free
+#pragma unroll
+      for (int u = 0; u < U; ++u) issue(t0 + NS - U + u);
+#pragma unroll
+      for (int u = 0; u < U; ++u) multiply(t0 + u);  // (tiles past the range are zeros)
     }
   }
   wait_vmcnt<0>();  // no LDS DMA outstanding at exit

@@ -10,33 +10,39 @@ namespace mcg {
 
 namespace {
 int64_t cdiv(int64_t x, int64_t y) { return (x + y - 1) / y; }
-// One round of tiles takes KT_US per 128-byte K tile and ROUND_US; stream-K's last
-// round adds FIXUP_US and a trip of its slots through the workspace.
-constexpr double KT_US_256_16BIT = 1.6, KT_US_256_8BIT = 0.85, KT_US_128 = 0.55, KT_US_64 = 0.38, ROUND_US = 4.0, FIXUP_US = 5.0;
-constexpr int64_t MIN_TILES_256 = 128;  // 256 x 256 tiles from which that form is faster
+// One round of tiles takes KT_US per 128-byte K tile and ROUND_US, most of it the
+// epilogue (from 500 x 4096 x 4096 to 8192^3); stream-K's last round adds FIXUP_US and
+// a trip of its slots through the workspace.  16-bit 5703 x 1344 x 4288: 138 tiles of
+// 256 x 256 take 140 us, 495 of 128 x 128 85; int8 5536 x 768 x 832: 66 take 27, 264 20.
+struct TileTime {
+  double kt_us, round_us;
+};
+constexpr TileTime TILE_256{1.45, 15.0}, TILE_128{0.5, 6.0}, TILE_64{0.38, 4.5};
+constexpr double FIXUP_US = 5.0;
 }  // namespace
 
 PipePlan plan_pipe(int dt, DenseArgs& a, int num_cu, int64_t ws_cap) {
   const int64_t nk = cdiv(a.K * (dt == DT_I8 ? 1 : 2), KT_BYTES);
-  auto whole = [&](int64_t tm, int64_t tn, double kt) {
-    return cdiv(cdiv(a.M, tm) * cdiv(a.N, tn), num_cu) * (kt * nk + ROUND_US);
+  PipePlan best{0, 0, 0.0};
+  auto consider = [&](int tile, int64_t ws, double us) {
+    if (best.tile == 0 || us < best.us) best = PipePlan{tile, ws, us};
   };
-  PipePlan p;
-  p.tile = cdiv(a.M, 256) * cdiv(a.N, 256) >= MIN_TILES_256 ? 256 : 128;
-  const double kt = p.tile == 128 ? KT_US_128 : dt == DT_I8 ? KT_US_256_8BIT : KT_US_256_16BIT;
-  p.us = whole(p.tile, p.tile, kt);
-  p.ws = plan_streamk(dt, a, num_cu, p.tile);
-  if (p.ws > 0 && p.ws <= ws_cap)
-    p.us = cdiv(a.dp_tiles, num_cu) * (kt * nk + ROUND_US) + kt * a.sk_iters + ROUND_US + FIXUP_US + 2.0 * p.ws / 4.5e6;
-  else p.ws = 0;
-  const double half = whole(64, 128, KT_US_64);
-  if (p.tile == 128 && half < p.us) {
-    p.tile = 64;
-    p.us = half;
-    p.ws = 0;
+  auto whole = [&](int64_t tm, int64_t tn, const TileTime& t) {
+    return cdiv(cdiv(a.M, tm) * cdiv(a.N, tn), num_cu) * (t.kt_us * nk + t.round_us);
+  };
+  for (int tile = 256; tile >= 128; tile /= 2) {
+    const TileTime& t = tile == 256 ? TILE_256 : TILE_128;
+    consider(tile, 0, whole(tile, tile, t));
+    const int64_t ws = plan_streamk(dt, a, num_cu, tile);
+    if (ws > 0 && ws <= ws_cap)
+      consider(tile, ws,
+               cdiv(a.dp_tiles, num_cu) * (t.kt_us * nk + t.round_us) + t.kt_us * a.sk_iters + t.round_us + FIXUP_US +
+                   2.0 * ws / 4.5e6);
   }
-  if (p.ws == 0) a.dp_tiles = a.sk_tiles = a.sk_wgs = 0;
-  return p;
+  consider(64, 0, whole(64, 128, TILE_64));
+  if (best.ws > 0) plan_streamk(dt, a, num_cu, best.tile);
+  else a.dp_tiles = a.sk_tiles = a.sk_wgs = 0;
+  return best;
 }
 
 // One 16-byte chunk of the destination per thread.

@@ -243,7 +243,7 @@ struct TileCost {
 
 // K ranges for `tiles` workgroups of nk K tiles each, from the time model
 //   max(alone * rounds, shared * workgroups per unit) * ceil(nk / s)
-//   + (s > 1 ? 7.5 + s * M * N * slot_us : fixed), in us,
+//   + (s > 1 ? 7.5 + s * M * N * slot_us : fixed * rounds), in us,
 // where a range's partial results make one trip through the workspace.
 inline int64_t plan_ranges(int64_t tiles, int64_t nk, int64_t out_elems, int num_cu, const TileCost& c,
                            int64_t max_splits, double* us) {
@@ -255,7 +255,7 @@ inline int64_t plan_ranges(int64_t tiles, int64_t nk, int64_t out_elems, int num
     if (s > 1 && cdiv(nk, cdiv(nk, s)) != s) continue;  // every range non-empty
     const int64_t per_cu = cdiv(tiles * s, num_cu), rounds = cdiv(per_cu, c.resident);
     const double kt = c.alone * (double)rounds > c.shared * (double)per_cu ? c.alone * (double)rounds : c.shared * (double)per_cu;
-    const double t = kt * (double)cdiv(nk, s) + (s > 1 ? SPLIT_FIXED_US : c.fixed) +
+    const double t = kt * (double)cdiv(nk, s) + (s > 1 ? SPLIT_FIXED_US : c.fixed * (double)rounds) +
                      (s > 1 ? (double)s * (double)out_elems * SLOT_US + SPLIT_US : 0.0);
     if (s == 1 || t < best_t) {
       best = s;
