@@ -6,9 +6,10 @@
 // added to the bias and rounded to D's type.
 //
 // General kernel: tiles of 128, 64 or 32 rows (general_rows) x 128 columns, 4
-// wavefronts, any size, pointer and leading dimension; the structure of dense_general.hpp with the loaders of tile_any.hpp.
-// K may be cut into ranges (few tiles, long K): each range leaves its int32 sums
-// in the workspace and a second kernel adds them and applies the epilogue.
+// wavefronts, any size, pointer and leading dimension; the structure of
+// dense_general.hpp with the loaders of tile_any.hpp.  K may be cut into
+// ranges (few tiles, long K): each range leaves its int32 sums in the workspace and a
+// second kernel adds them and applies the epilogue.
 #include <algorithm>
 
 #include "scaled_epilogue.hpp"
