@@ -365,8 +365,8 @@ static hipError_t launch_panels(int dtA, int la, const GradArgs& a, int num_cu, 
   char* slots = hi + (two ? 2 : 1) * panel_bytes(a);
   hipError_t e = hipSuccess;
   if (a.lda2)
-    e = la == LAYOUT_K ? launch_align_rows(a.A, a.lda * 2, a.M, a.K * 2, a.ws, a.lda2 * 2, a.M, s)
-                       : launch_align_rows(a.A, a.lda * 2, a.K, a.M * 2, a.ws, a.lda2 * 2, a.K, s);
+    e = la == LAYOUT_K ? launch_align_rows({a.A, a.lda * 2, a.M, a.K * 2, (char*)a.ws, a.lda2 * 2, a.M}, s)
+                       : launch_align_rows({a.A, a.lda * 2, a.K, a.M * 2, (char*)a.ws, a.lda2 * 2, a.K}, s);
   for (int64_t n0 = 0; n0 < a.N && e == hipSuccess; n0 += a.panel_n) {
     const int64_t nc = std::min(a.panel_n, a.N - n0);
     e = dtA == DT_BF16 ? launch_widen<OpBF16>(a, n0, nc, hi, lo, s) : launch_widen<OpF16>(a, n0, nc, hi, lo, s);

@@ -194,7 +194,8 @@ double plan_panels(int lb, ScaledArgs& a, int num_cu, int64_t ws_bytes, int64_t*
   ScaledArgs d = panel_args(lb, a, 0, a.panel_n);
   const PipePlan pp = plan_pipe(DT_I8, d, num_cu, ws_bytes - bytes);
   *used = bytes + pp.ws;
-  return pass_us(2.0 * fixed) + cdiv(a.N, a.panel_n) * (pass_us(2.0 * panel_bytes(lb, a)) + pp.us);
+  constexpr double BYTE_US = 1 / 4.5e6, LAUNCH_US = 4.0;  // of the copies
+  return 2.0 * fixed * BYTE_US + cdiv(a.N, a.panel_n) * (2.0 * panel_bytes(lb, a) * BYTE_US + LAUNCH_US + pp.us);
 }
 }  // namespace
 
@@ -266,13 +267,15 @@ static hipError_t launch_pipe(int lb, const ScaledArgs& a, hipStream_t s) {
 }
 
 static hipError_t launch_panels(int lb, const ScaledArgs& a, int num_cu, hipStream_t s) {
-  hipError_t e = launch_align_rows(a.A, a.lda, a.M, a.K, a.ws, a.kp, a.M, s);
+  hipError_t e = hipSuccess;
+  const AlignRows copy_a{a.A, a.lda, a.M, a.K, (char*)a.ws, a.kp, a.M};
   const int64_t bytes = a.M * a.kp + panel_bytes(lb, a);
   for (int64_t n0 = 0; n0 < a.N && e == hipSuccess; n0 += a.panel_n) {
     const int64_t nc = std::min(a.panel_n, a.N - n0);
     ScaledArgs d = panel_args(lb, a, n0, nc);
-    e = lb == LAYOUT_K ? launch_align_rows(a.B + n0 * a.ldb, a.ldb, nc, a.K, (void*)d.B, a.kp, nc, s)
-                       : launch_align_rows(a.B + n0, a.ldb, a.K, nc, (void*)d.B, a.ldb2, a.kp, s);
+    const AlignRows copy_b = lb == LAYOUT_K ? AlignRows{a.B + n0 * a.ldb, a.ldb, nc, a.K, (char*)d.B, a.kp, nc}
+                                            : AlignRows{a.B + n0, a.ldb, a.K, nc, (char*)d.B, a.ldb2, a.kp};
+    e = n0 == 0 ? launch_align_rows(copy_a, s, &copy_b) : launch_align_rows(copy_b, s);
     if (e != hipSuccess) break;
     d.ws = (char*)a.ws + bytes;
     d.tile = plan_pipe(DT_I8, d, num_cu, a.ws_bytes - bytes).tile;

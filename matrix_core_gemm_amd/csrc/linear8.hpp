@@ -111,10 +111,15 @@ struct PipePlan {
 // 16-bit A in layoutA, MN-contiguous B, 64 x 128 tiles.
 hipError_t launch_fast_half(int dtA, int layoutA, const DenseArgs& a, hipStream_t s);
 PipePlan plan_pipe(int dt, DenseArgs& a, int num_cu, int64_t ws_cap);
-// Rows of row_bytes bytes, lds apart, to rows of ldd bytes (a multiple of 16), zeros
-// past row_bytes and past `rows` up to rows_d.
-hipError_t launch_align_rows(const void* src, int64_t lds, int64_t rows, int64_t row_bytes, void* dst, int64_t ldd,
-                             int64_t rows_d, hipStream_t s);
+// A copy of rows of row_bytes bytes, lds apart, to rows of ldd bytes (a multiple of
+// 16), zeros past row_bytes and past `rows` up to rows_d.
+struct AlignRows {
+  const char* src;
+  int64_t lds, rows, row_bytes;
+  char* dst;
+  int64_t ldd, rows_d;
+};
+hipError_t launch_align_rows(const AlignRows& a, hipStream_t s, const AlignRows* second = nullptr);
 // Time of a pass that moves `bytes` at the rate of a copy, with its launch, in us.
 inline double pass_us(double bytes) { return 3.0 + bytes / 5.5e6; }
 

@@ -45,22 +45,27 @@ PipePlan plan_pipe(int dt, DenseArgs& a, int num_cu, int64_t ws_cap) {
   return best;
 }
 
-// One 16-byte chunk of the destination per thread.
-__global__ __launch_bounds__(256) void align_rows_kernel(const char* src, int64_t lds, int64_t rows, int64_t row_bytes,
-                                                         char* dst, int64_t ldd, uint32_t cpr, uint32_t chunks) {
+// One 16-byte chunk of a destination per thread: first the first copy's chunks, then
+// the second's (both operands of a product in one launch: 1024^3, rows 1027 apart, 14.5
+// us with two launches, 12.8 with one).
+__device__ __forceinline__ void align_chunk(const AlignRows& a, uint32_t i) {
+  const uint32_t cpr = (uint32_t)(a.ldd / 16), r = i / cpr, c = i % cpr;
+  const int64_t left = r < a.rows ? a.row_bytes - 16 * (int64_t)c : 0;
+  *(i32x4*)(a.dst + r * a.ldd + 16 * (int64_t)c) =
+      load_chunk(a.src, a.src + r * a.lds + 16 * (int64_t)c, (int)min(left, (int64_t)16));
+}
+__global__ __launch_bounds__(256) void align_rows_kernel(AlignRows a, AlignRows b, uint32_t chunks_a, uint32_t chunks) {
   const uint32_t i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= chunks) return;
-  const uint32_t r = i / cpr, c = i % cpr;
-  const int64_t left = r < rows ? row_bytes - 16 * (int64_t)c : 0;
-  *(i32x4*)(dst + r * ldd + 16 * (int64_t)c) = load_chunk(src, src + r * lds + 16 * (int64_t)c, (int)min(left, (int64_t)16));
+  if (i < chunks_a) align_chunk(a, i);
+  else if (i < chunks) align_chunk(b, i - chunks_a);
 }
 
-hipError_t launch_align_rows(const void* src, int64_t lds, int64_t rows, int64_t row_bytes, void* dst, int64_t ldd,
-                             int64_t rows_d, hipStream_t s) {
-  const int64_t cpr = ldd / 16, chunks = cpr * rows_d;
+hipError_t launch_align_rows(const AlignRows& a, hipStream_t s, const AlignRows* second) {
+  const AlignRows b = second ? *second : AlignRows{};
+  const int64_t chunks_a = a.ldd / 16 * a.rows_d, chunks = chunks_a + b.ldd / 16 * b.rows_d;
   if (chunks > 0xffffff00) return hipErrorInvalidValue;  // (a launch holds less than 2^32 threads)
-  hipLaunchKernelGGL(align_rows_kernel, dim3((unsigned)cdiv(chunks, 256)), dim3(256), 0, s, (const char*)src, lds, rows,
-                     row_bytes, (char*)dst, ldd, (uint32_t)cpr, (uint32_t)chunks);
+  hipLaunchKernelGGL(align_rows_kernel, dim3((unsigned)cdiv(chunks, 256)), dim3(256), 0, s, a, b, (uint32_t)chunks_a,
+                     (uint32_t)chunks);
   return hipGetLastError();
 }
 
