@@ -347,7 +347,7 @@ int decompress24_host(int dtype, int64_t M, int64_t K, const void* A_compressed,
  *
  * rmsnorm_quant -- the root-mean-square norm of a sum, in 8 bits:
  *     h = x + r,  rstd = (mean(h^2) + eps)^(-1/2),  y = h * weight * rstd
- *     scale = max|y| / 127,  q = rint(y / scale)      (ties to even)
+ *     scale = max|y| / 127,  q = rint(127 y / max|y|)      (ties to even)
  * for each of M rows of N channels.
  *
  * dtype         : MCG_BF16, MCG_F16 or MCG_F32, of X, R, weight and H.
@@ -358,7 +358,11 @@ int decompress24_host(int dtype, int64_t M, int64_t K, const void* A_compressed,
  *                 pointer and leading dimension); other overlaps are undefined.
  * Q, ldq, scale : codes (-127..127) and M scales.
  * rstd          : M values, or NULL (kept for rmsnorm_backward).
- * Squares and sums are binary32, taken of the sum h before it is rounded.  A row
+ * Squares and sums are binary32, taken of the sum h before it is rounded.  The
+ * quotient 127 y / max|y| is rounded to binary32 before it is to an integer, and
+ * formed of binary32 values h * weight (rstd cancels): of 16-bit X without R and
+ * weight the codes are those of the exact quotient, else of one within 2^-21 of
+ * it (relative).  A row
  * whose y is all zero has scale 0; a row with a NaN or an infinity, or whose
  * squares leave binary32, has scale NaN and codes 0.  N == 0 gives scale 0.
  */
@@ -393,7 +397,8 @@ int64_t mcg_rmsnorm_backward_workspace_bytes(int64_t M, int64_t N);
 
 /*
  * quantize_rows / dequantize_rows -- the 8-bit checkpoint of an activation:
- * scale = max|x| / 127 and q = rint(x / scale) for each row, and the values
+ * scale = max|x| / 127 and q = rint(127 x / max|x|) for each row (ties to even,
+ * the quotient rounded to binary32 first: exact for 16-bit X), and the values
  * scale * q rounded once to dtypeD (MCG_BF16, MCG_F16 or MCG_F32).  Rows of
  * zeros, NaN and infinities as for rmsnorm_quant (the values of a row with
  * scale NaN are NaN).

@@ -3,9 +3,9 @@
 // (dequantize_rows).
 //
 //   h = x + r,  rstd = (mean(h^2) + eps)^(-1/2),  y = h * w * rstd
-//   scale = max|y| / 127,  q = rint(y / scale)
+//   scale = max|y| / 127,  q = rint(127 y / max|y|)
 //
-// rstd > 0 is common to the row, so max|y| = rstd * max|h w| and y / scale =
+// rstd > 0 is common to the row, so max|y| = rstd * max|h w| and y / (max|y| / 127) =
 // 127 h w / max|h w|: both reductions (the sum of squares and the largest
 // |h w|) run over the same values at once, and the codes need no rstd.  A row is
 // read once and kept in registers between its reductions and its stores.
@@ -48,12 +48,12 @@ __device__ __forceinline__ void row_reduce(float& ss, uint32_t& top, int phase) 
   }
 }
 
-// A row's statistics from its reductions: the factor of its codes (after the
-// exact factor pre, which keeps 127 / max in range for a row of tiny values),
-// its scale and rstd.  A row with a NaN or an infinity, or whose squares
-// overflow, gets the scale NaN and codes 0; a row of zeros the scale 0.
+// A row's statistics from its reductions: the factor 127 / max of its codes, its
+// scale and rstd.  A row with a NaN or an infinity, or whose squares overflow, gets
+// the scale NaN and codes 0; a row of zeros the scale 0.
 struct RowStat {
-  float pre, inv, scale, rstd;
+  double inv;
+  float scale, rstd;
 };
 template <bool NORM>
 __device__ __forceinline__ RowStat row_stat(float ss, uint32_t top, int64_t n, float eps) {
@@ -62,20 +62,26 @@ __device__ __forceinline__ RowStat row_stat(float ss, uint32_t top, int64_t n, f
   s.rstd = 1.0f;
   if constexpr (NORM) s.rstd = 1.0f / __builtin_sqrtf((n > 0 ? ss / (float)n : 0.0f) + eps);
   const bool finite = top < 0x7f800000u && (!NORM || ss < __builtin_inff());
-  s.pre = t < 0x1p-100f ? 0x1p100f : 1.0f;
-  s.inv = finite && t > 0.0f ? QMAX / (t * s.pre) : 0.0f;
+  s.inv = finite && t > 0.0f ? (double)QMAX / (double)t : 0.0;
   if (!finite) s.scale = __builtin_nanf("");
   else s.scale = t > 0.0f ? t * s.rstd / QMAX : 0.0f;
   return s;
 }
 
-// Codes of eight values: nearest even, at most 127 in magnitude (127 * t / t may
-// round past it by one unit).  Adding 1.5 * 2^23 rounds to an integer whose two's
-// complement is in the low bits of the sum (5 instead of 9 instructions a code).
+// Codes of eight values: 127 y / max|y| in binary64, rounded to binary32 and then to
+// the nearest integer, ties to even.  The binary64 product is off by at most 2^-52 of
+// its value, so the binary32 one is that of the exact quotient but within 2^-52 of the
+// middle of two: a tie of integers (63.5 for half the largest value, common in 16-bit
+// rows) stays one, and no other quotient of 16-bit values comes nearer to one than
+// 2^-20, so that their codes are exact.  (As y * (127 / max) in binary32, 632 of 16384
+// codes of f16 rows that hold that half were the other neighbour.)
+// At most 127 in magnitude: 127 (1 + 2^-52) rounds to it.  Adding 1.5 * 2^23 rounds to
+// an integer whose two's complement is in the low bits of the sum; with the two
+// conversions four instructions a code, as in binary32 with a clamp.
 // inv == 0 (see RowStat) gives zeros: the values may then be infinite or NaN.
 __device__ __forceinline__ Raw8<DT_I8> codes8(const float (&y)[8], const RowStat& s) {
   Raw8<DT_I8> v;
-  if (s.inv == 0.0f) {
+  if (s.inv == 0.0) {
     v.w[0] = v.w[1] = 0;
     return v;
   }
@@ -83,8 +89,7 @@ __device__ __forceinline__ Raw8<DT_I8> codes8(const float (&y)[8], const RowStat
   for (int i = 0; i < 2; ++i) {
     uint32_t b[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      b[e] = bit_cast<uint32_t>(__builtin_amdgcn_fmed3f(y[4 * i + e] * s.pre * s.inv, -QMAX, QMAX) + 12582912.0f);
+    for (int e = 0; e < 4; ++e) b[e] = bit_cast<uint32_t>((float)((double)y[4 * i + e] * s.inv) + 12582912.0f);
     const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
     v.w[i] = lo | hi;
   }

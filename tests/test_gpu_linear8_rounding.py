@@ -1,0 +1,73 @@
+"""Codes of 8-bit rows at and next to a tie, against exact values.  Sizes: every form of the row kernels (rows shorter
+than a vector, in a wavefront's or a workgroup's registers, and read twice)."""
+import numpy as np
+import pytest
+import torch
+
+import linear8_ref as ref
+from gpu_util import need_gpu
+from linear8_ref import DT, U32
+
+pytestmark = pytest.mark.gpu
+
+# rows, columns
+FORMS = [(2048, 5), (2048, 8), (300, 300), (300, 700), (300, 1500), (300, 3000), (300, 5000), (40, 8000), (300, 8000),
+         (40, 12000), (20, 20000)]
+
+
+def rows_with_ties(dt, M, N):
+    """Rows with the largest values' mantissas in turn (all of them from 1024 rows on for
+    f16, 128 for bf16), plus and minus half of it, and values of all sizes below."""
+    t = DT[dt]
+    bits = 10 if dt == "f16" else 7
+    i = torch.arange(M)
+    top = (2 ** bits + (i * 37) % 2 ** bits).double() * 2.0 ** (i % 9 - 12).double()
+    x = (top[:, None] * torch.from_numpy(np.random.default_rng(N).uniform(-1, 1, (M, N)))).to(t)
+    lead = torch.stack([top, top / 2, -top / 2], 1).to(t)
+    x[:, :3] = lead
+    if N > 8:
+        x[:, -3:] = lead
+    return x
+
+
+def exact_quotients(x):
+    """127 x / max|x|: a tie is exact in binary64 (127 x and the quotient are), and every
+    other quotient of two 16-bit values is at least 2^-20 from one."""
+    top = x.double().abs().amax(1, keepdim=True)
+    return 127.0 * x.double() / top
+
+
+@pytest.mark.parametrize("norm", [False, True], ids=["rows", "norm"])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("shape", FORMS, ids=str)
+def test_codes_of_16_bit_rows_are_the_nearest(dt, shape, norm):
+    mcg = need_gpu()
+    M, N = shape
+    x = rows_with_ties(dt, M, N)
+    X, Q, scale = x.cuda(), torch.empty(M, N, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+    if norm:  # without weights and residual the codes do not depend on the norm
+        mcg.rmsnorm_quant(dt, M, N, X, N, None, 0, None, 1e-5, None, 0, Q, N, scale)
+    else:
+        mcg.quantize_rows(dt, M, N, X, N, Q, N, scale)
+    want = exact_quotients(x).round()  # ties to even
+    bad = Q.cpu().double() != want
+    assert not bool(bad.any()), f"{int(bad.sum())} of {bad.numel()} codes, first at {bad.nonzero()[0].tolist()}"
+
+
+@pytest.mark.parametrize("shape", FORMS, ids=str)
+def test_codes_of_other_rows_are_the_nearest_but_for_roundings(shape):
+    mcg = need_gpu()
+    M, N = shape
+    Q, scale = torch.empty(M, N, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+    # binary32: the quotient is rounded to binary32 before it is to an integer
+    x = ref.rand(N, M, N, gain=3).float()
+    mcg.quantize_rows("f32", M, N, x.cuda(), N, Q, N, scale)
+    d = (Q.cpu().double() - exact_quotients(x)).abs().max()
+    assert d <= 0.5 + 127 * U32, float(d)
+    # a norm of a sum with weights: h and h w (of the value and of the largest) are rounded too
+    h, r = ref.rand(N + 1, M, N).to(torch.bfloat16), ref.rand(N + 2, M, N).to(torch.bfloat16)
+    w = (1 + 0.2 * ref.rand(N + 3, N)).to(torch.bfloat16)
+    mcg.rmsnorm_quant("bf16", M, N, h.cuda(), N, r.cuda(), N, w.cuda(), 1e-5, None, 0, Q, N, scale)
+    y = (h.double() + r.double()) * w.double()
+    d = (Q.cpu().double() - exact_quotients(y)).abs().max()
+    assert d <= 0.5 + 127 * 5 * U32, float(d)
