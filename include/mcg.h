@@ -363,8 +363,9 @@ int decompress24_host(int dtype, int64_t M, int64_t K, const void* A_compressed,
  * formed of binary32 values h * weight (rstd cancels): of 16-bit X without R and
  * weight the codes are those of the exact quotient, else of one within 2^-21 of
  * it (relative).  A row
- * whose y is all zero has scale 0; a row with a NaN or an infinity, or whose
- * squares leave binary32, has scale NaN and codes 0.  N == 0 gives scale 0.
+ * whose y is all zero has scale 0.  A row with a NaN or an infinity, whose squares
+ * or products h * weight overflow, or (possible with an eps below it only) whose
+ * mean(h^2) + eps is under 2^-126, has scale NaN and codes 0.  N == 0 gives scale 0.
  */
 int rmsnorm_quant(int dtype, int64_t M, int64_t N, const void* X, int64_t ldx, const void* R, int64_t ldr,
                   const void* weight, double eps, void* H, int64_t ldh, int8_t* Q, int64_t ldq, float* scale,

@@ -49,8 +49,10 @@ __device__ __forceinline__ void row_reduce(float& ss, uint32_t& top, int phase) 
 }
 
 // A row's statistics from its reductions: the factor 127 / max of its codes, its
-// scale and rstd.  A row with a NaN or an infinity, or whose squares overflow, gets
-// the scale NaN and codes 0; a row of zeros the scale 0.
+// scale and rstd.  A row with a NaN or an infinity, whose squares overflow, or whose
+// mean square plus eps is below the normal numbers (an eps of 0: squares lose their
+// bits there, and rstd ends infinite) gets the scale NaN and codes 0; a row of zeros
+// the scale 0.
 struct RowStat {
   double inv;
   float scale, rstd;
@@ -60,8 +62,12 @@ __device__ __forceinline__ RowStat row_stat(float ss, uint32_t top, int64_t n, f
   RowStat s;
   const float t = bit_cast<float>(top);
   s.rstd = 1.0f;
-  if constexpr (NORM) s.rstd = 1.0f / __builtin_sqrtf((n > 0 ? ss / (float)n : 0.0f) + eps);
-  const bool finite = top < 0x7f800000u && (!NORM || ss < __builtin_inff());
+  bool finite = top < 0x7f800000u;
+  if constexpr (NORM) {
+    const float mean = (n > 0 ? ss / (float)n : 0.0f) + eps;
+    s.rstd = 1.0f / __builtin_sqrtf(mean);
+    finite = finite && ss < __builtin_inff() && (mean >= 0x1p-126f || top == 0);
+  }
   s.inv = finite && t > 0.0f ? (double)QMAX / (double)t : 0.0;
   if (!finite) s.scale = __builtin_nanf("");
   else s.scale = t > 0.0f ? t * s.rstd / QMAX : 0.0f;

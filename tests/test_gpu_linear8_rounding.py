@@ -1,5 +1,6 @@
-"""Codes of 8-bit rows at and next to a tie, against exact values.  Sizes: every form of the row kernels (rows shorter
-than a vector, in a wavefront's or a workgroup's registers, and read twice)."""
+"""Codes of 8-bit rows at and next to a tie, and rows whose squares leave binary32,
+against exact values.  Sizes: every form of the row kernels (rows shorter than a vector,
+in a wavefront's or a workgroup's registers, and read twice)."""
 import numpy as np
 import pytest
 import torch
@@ -71,3 +72,30 @@ def test_codes_of_other_rows_are_the_nearest_but_for_roundings(shape):
     y = (h.double() + r.double()) * w.double()
     d = (Q.cpu().double() - exact_quotients(y)).abs().max()
     assert d <= 0.5 + 127 * 5 * U32, float(d)
+
+
+@pytest.mark.parametrize("N", [5, 300, 3000, 12000, 20000])
+def test_rows_whose_mean_square_is_below_binary32(N):
+    """With eps 0 a row can have a mean square that is no normal binary32 number: it is
+    marked like one whose squares overflow.  With an eps it is a row like any other."""
+    mcg = need_gpu()
+    gains = [1e-42, 1e-36, 1e-25, 1e-21, 1e-18, 1e-3, 1.0]
+    M = len(gains) + 1
+    x = torch.stack([ref.rand(i, N) for i in range(M)]).float()
+    x = x.sign() * x.abs().clamp(0.25, 4.0)
+    for i, g in enumerate(gains):
+        x[i] = (x[i].double() * g).float()
+    x[M - 1] = 0
+    Q, scale, rstd = torch.empty(M, N, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda"), torch.empty(M, device="cuda")
+    mcg.rmsnorm_quant("f32", M, N, x.cuda(), N, None, 0, None, 0.0, None, 0, Q, N, scale, rstd)
+    q, s = Q.cpu(), scale.cpu()
+    assert bool(torch.isnan(s[:4]).all()) and not q[:4].any(), s
+    assert float(s[M - 1]) == 0 and not q[M - 1].any()
+    _, y, rs = ref.rmsnorm(x[4:M - 1], None, None, 0.0)
+    top = y.abs().amax(1) / 127
+    assert bool(((s[4:M - 1].double() - top).abs() <= 2.0 ** -16 * top).all())
+    assert bool(((rstd[4:M - 1].cpu().double() - rs).abs() <= 2.0 ** -17 * rs).all())
+    assert bool(((q[4:M - 1].double() - y / top[:, None]).abs() <= 0.5 + 127 * 2 * U32).all())
+    mcg.rmsnorm_quant("f32", M, N, x.cuda(), N, None, 0, None, 1e-5, None, 0, Q, N, scale, rstd)
+    q, s = Q.cpu(), scale.cpu()
+    assert bool(torch.isfinite(s).all()) and bool((q[:M - 1].abs().amax(1) == 127).all())
