@@ -42,6 +42,11 @@ __device__ __forceinline__ float row_sum(float x, int phase) {
   return x;
 }
 
+// c of the formulas: rstd^2 / n * sum, one factor rstd at a time (its square leaves
+// binary32 for rows of about 1e-19 and less, or 1e19 and more; sum * rstd has the size
+// of n g).
+__device__ __forceinline__ float row_factor(float sum, float rstd, int64_t n) { return sum * rstd / (float)n * rstd; }
+
 template <int DT, int DTX>
 __device__ __forceinline__ void load_x(const NormGradArgs& p, int64_t row, int64_t c, float (&x)[8]) {
   widen8<DTX>(load8<DTX>(p.X + row * p.ldx * elem_size<DTX>(), c, p.N), x);
@@ -132,7 +137,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(NormGr
       }
     }
     sum = row_sum<TPR>(sum, phase);
-    const float k = sum * (rs * rs) / (float)p.N;
+    const float k = row_factor(sum, rs, p.N);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float o[8];
@@ -192,7 +197,7 @@ __global__ __launch_bounds__(1024) void norm_grad_long_kernel(NormGradArgs p) {
       for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(g[e], x[e], sum);
     }
     sum = row_sum<1024>(sum, phase);
-    const float k = sum * (rstd * rstd) / (float)p.N;
+    const float k = row_factor(sum, rstd, p.N);
     for (int64_t c = (int64_t)threadIdx.x * 8; c < p.N; c += 8192) {
       float g[8], x[8];
       load(c, g, x);

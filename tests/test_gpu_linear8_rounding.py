@@ -1,6 +1,7 @@
-"""Codes of 8-bit rows at and next to a tie, and rows whose squares leave binary32,
-against exact values.  Sizes: every form of the row kernels (rows shorter than a vector,
-in a wavefront's or a workgroup's registers, and read twice)."""
+"""Codes of 8-bit rows at and next to a tie, rows whose squares leave binary32, and the
+gradient of rows far from one, against exact values.  Sizes: every form of the row
+kernels (rows shorter than a vector, in a wavefront's or a workgroup's registers, and
+read twice)."""
 import numpy as np
 import pytest
 import torch
@@ -99,3 +100,33 @@ def test_rows_whose_mean_square_is_below_binary32(N):
     mcg.rmsnorm_quant("f32", M, N, x.cuda(), N, None, 0, None, 1e-5, None, 0, Q, N, scale, rstd)
     q, s = Q.cpu(), scale.cpu()
     assert bool(torch.isfinite(s).all()) and bool((q[:M - 1].abs().amax(1) == 127).all())
+
+
+@pytest.mark.parametrize("x8", [False, True], ids=["x", "x8"])
+@pytest.mark.parametrize("N", [5, 300, 700, 1500, 3000, 5000, 8000, 12000, 20000])
+def test_gradient_of_rows_far_from_one(N, x8):
+    """Rows whose rstd squared is no normal binary32 number (or none at all): the gradient
+    is, and is held to the same bound as any row's."""
+    mcg = need_gpu()
+    gains = [1e-30, 1e-22, 1e-3, 1.0, 1e17, 1e22, 1e30]
+    M = len(gains)
+    g = torch.tensor(gains, dtype=torch.float64)
+    dy = ref.rand(N, M, N).float()
+    if x8:
+        x, scale = ref.codes(N + 1, M, N), (g * 0.02).float()
+        xv = x.double() * scale.double()[:, None]
+    else:
+        x, scale = (ref.rand(N + 1, M, N) * g[:, None]).float(), None
+        xv = x.double()
+    rstd = ref.rmsnorm(xv, None, None, 0.0)[2].float()
+    dX = torch.empty(M, N, device="cuda")
+    mcg.rmsnorm_backward("f32", "i8" if x8 else "f32", M, N, dy.cuda(), N, x.cuda(), N, scale.cuda() if x8 else None, None,
+                         rstd.cuda(), None, 0, dX, N, None)
+    dx = ref.rmsnorm_backward(dy, xv, None, rstd, None)[0]
+    # as in test_rmsnorm_backward of the layer's tests, with binary32 results
+    r = rstd.double()[:, None]
+    c = r.square() * (dy.double() * xv).abs().mean(1, keepdim=True)
+    tol = (64 + N // 1024) * U32 * r * (dy.double().abs() + c * xv.abs()) + U32 * dx.abs() + ref.SUB["f32"]
+    d = (dX.cpu().double() - dx).abs()
+    ok = d <= tol
+    assert bool(ok.all()), [(gains[i], float((d[i] / tol[i]).nan_to_num(1e30).max())) for i in range(M) if not bool(ok[i].all())]
