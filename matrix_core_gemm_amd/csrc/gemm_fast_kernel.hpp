@@ -707,14 +707,13 @@ void gemm_fast_kernel(typename KernelTypes<Op>::Args p) {
       }
       if (pc > 0) barrier_lds();  // the previous piece's epilogue is done with the LDS
       const bool whole = kbeg == 0 && kcnt == nk_all;
-      Dst d = whole_tile(tm, tn);
-      if (!whole) {
-        const EpiDst slot{(char*)p.ws + piece * (int64_t)(TB * TB * 4), nullptr, TB, TB, TB, 0, 0,
-                          1.0f, 0.0f, 1, 0, 0, 1, OUT_32};
-        if constexpr (SCALED) d = Dst{slot, nullptr, nullptr, nullptr};
-        else d = slot;
-      }
-      work(tm, tn, kbeg, kcnt, d);
+      // (one expression: with the slot assigned over the tile's destination the int8
+      // instance of two K-contiguous operands spilled 127 registers instead of 80, and
+      // 4096 x 4352 x 4096 took 95.8 instead of 94.7 us)
+      const EpiDst slot{(char*)p.ws + piece * (int64_t)(TB * TB * 4), nullptr, TB, TB, TB, 0, 0,
+                        1.0f, 0.0f, 1, 0, 0, 1, OUT_32};
+      if constexpr (SCALED) work(tm, tn, kbeg, kcnt, whole ? whole_tile(tm, tn) : Dst{slot, nullptr, nullptr, nullptr});
+      else work(tm, tn, kbeg, kcnt, whole ? whole_tile(tm, tn) : slot);
       it += kcnt;
       ++piece;
     }
