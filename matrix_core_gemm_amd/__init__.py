@@ -4,7 +4,9 @@ Argument marshalling only: every function has the C entry point's name and
 argument order, turns torch tensors into device pointers, defaults the stream
 to torch's current stream, and raises ``MCGError`` on a non-zero status.  All
 arithmetic runs in the HIP kernels of ``_libmcg.so``; there is no fallback.
-If the library has not been built, importing this package fails.
+If the library has not been built, importing this package fails.  The entry points
+of the 8-bit linear layer are called through a C extension (csrc/pycall.c) where it
+is built for this Python, else through ctypes like the others.
 
 dtype and layout arguments take the C enum values or their names:
   dtypes : "bf16", "f16", "i8", "e4m3", "e5m2", "f32", "i32", "f64"
@@ -14,6 +16,7 @@ dtype and layout arguments take the C enum values or their names:
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 import torch  # loaded first so the library binds to torch's HIP runtime
@@ -54,7 +57,10 @@ if not os.path.exists(LIB_PATH):
                       "(or __graft_entry__.build()); there is no non-GPU fallback")
 
 _lib = ctypes.CDLL(LIB_PATH)
-from . import _mcgcall  # noqa: E402  (calls into the same library)
+try:
+    from . import _mcgcall  # (calls into the same library)
+except ImportError:
+    _mcgcall = None  # not built, or for another Python: ctypes calls it (below)
 
 _i32, _i64, _dbl, _f32, _vp = ctypes.c_int, ctypes.c_int64, ctypes.c_double, ctypes.c_float, ctypes.c_void_p
 _lib.gemm_dense.argtypes = [_i32, _i32, _i32, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64,
@@ -164,7 +170,59 @@ def _check(fn: str, status: int) -> None:
         raise MCGError(fn, status)
 
 
-_mcgcall.setup(DTYPES, LAYOUTS, _stream, _raw_stream, _raw_device)
+class _CtypesCalls:
+    """csrc/pycall.c's calls through ctypes: positional arguments in the C order, the
+    stream last, converted by kind -- d dtype, l layout, i integer, f float, p device
+    address, b bytes of the workspace before it, s stream.  Returns the status."""
+
+    KINDS = {"rmsnorm_quant": "diipipipfpipipps", "rmsnorm_backward": "ddiipipippppipippbs", "quantize_rows": "diipipips",
+             "dequantize_rows": "diipippis", "gemm_i8_scaled": "liiipippipppidpbs", "gemm_grad_i8": "dliiipipipppidfpbs"}
+
+    def __getattr__(self, name):
+        kinds, fn = self.KINDS[name], getattr(_lib, name)
+
+        def call(*args):
+            if len(args) != len(kinds):
+                raise TypeError(f"{name} takes {len(kinds)} arguments ({len(args)} given)")
+            return fn(*(getattr(self, "_" + k)(a, args[i - 1]) for i, (k, a) in enumerate(zip(kinds, args))))
+        return call
+
+    @staticmethod
+    def _i(v, _=None):
+        v = operator.index(v)
+        if not -1 << 63 <= v < 1 << 63:
+            raise OverflowError("integer too large for 64 bits")
+        return v
+
+    def _d(self, v, _):
+        return DTYPES[v] if isinstance(v, str) else self._i(v)
+
+    def _l(self, v, _):
+        return LAYOUTS[v] if isinstance(v, str) else self._i(v)
+
+    @staticmethod
+    def _f(v, _):
+        if isinstance(v, str):
+            raise TypeError("must be real number, not str")
+        return float(v)
+
+    @staticmethod
+    def _p(v, _):
+        return v if v is None or isinstance(v, int) else v.data_ptr()
+
+    def _b(self, v, workspace):
+        v = self._i(v)
+        return workspace.nbytes if v == 0 and not (workspace is None or isinstance(workspace, int)) else v
+
+    @staticmethod
+    def _s(v, _):
+        return _stream(v)
+
+
+if _mcgcall is None:
+    _mcgcall = _CtypesCalls()
+else:
+    _mcgcall.setup(DTYPES, LAYOUTS, _stream, _raw_stream, _raw_device)
 
 
 def gemm_dense(dtypeA, dtypeB, layoutA, layoutB, M, N, K, A, lda, B, ldb, C, D, ldc, dtypeD,

@@ -2,8 +2,9 @@
 
 Every source is compiled by hipcc for gfx950 only; objects go to
 matrix_core_gemm_amd/_build/ and are linked into one shared library that the
-Python binding loads with ctypes.  _mcgcall.so (csrc/pycall.c, plain C) calls the
-small operators in it without ctypes.
+Python binding loads with ctypes.  _mcgcall (csrc/pycall.c, plain C, named for the
+Python that it is built for) calls the small operators in it without ctypes; where it
+cannot be built (no C compiler or no Python headers) they go through ctypes too.
 """
 from __future__ import annotations
 
@@ -16,7 +17,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "_libmcg.so")
-CALL = os.path.join(HERE, "_mcgcall.so")
+CALL = os.path.join(HERE, "_mcgcall" + sysconfig.get_config_var("EXT_SUFFIX"))
 CC = os.environ.get("CC", "gcc")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -85,11 +86,19 @@ def build(force: bool = True, verbose: bool = False) -> str:
     return LIB
 
 
-def build_call() -> str:
+def build_call() -> str | None:
+    """The C extension, or None with a message where it cannot be built."""
+    for old in (CALL, os.path.join(HERE, "_mcgcall.so")):  # (a stale one would be imported; the second name fits any Python)
+        if os.path.exists(old):
+            os.remove(old)
     tmp = CALL + ".tmp"
-    subprocess.check_call([CC, "-O2", "-std=gnu11", "-Wall", "-shared", "-fPIC", "-I" + sysconfig.get_paths()["include"],
-                           os.path.join(CSRC, "pycall.c"), "-o", tmp, "-L" + HERE, "-l:" + os.path.basename(LIB),
-                           "-Wl,-rpath,$ORIGIN"])
+    cmd = [CC, "-O2", "-std=gnu11", "-Wall", "-shared", "-fPIC", "-I" + sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "pycall.c"), "-o", tmp, "-L" + HERE, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN"]
+    try:
+        subprocess.check_call(cmd)
+    except (OSError, subprocess.CalledProcessError) as e:
+        sys.stderr.write(f"_mcgcall is not built ({e}); the binding calls the small operators through ctypes\n")
+        return None
     os.replace(tmp, CALL)
     return CALL
 
