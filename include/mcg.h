@@ -516,7 +516,15 @@ int mcg_validate_grad_i8(int dtypeA, int layoutA, int64_t M, int64_t N, int64_t 
    mcg_dense_splits: the number of K ranges (1 = no split) gemm_dense uses
      with exactly these arguments.
    mcg_sparse24_path: 1 if gemm_sparse24 runs the 256 x 256 pipelined kernel,
-     0 for the general one. */
+     0 for the general one.
+   mcg_i8_scaled_path, mcg_grad_i8_path: the kernel of gemm_i8_scaled and
+     gemm_grad_i8 with a workspace of workspace_bytes: 0 general kernel; 1, 6
+     and 7 the pipelined kernel with 256 x 256, 128 x 128 and 64 x 128 tiles; 4
+     the streaming kernel; 16 one output per thread (operands of under 16
+     bytes); -1 for an empty product or sizes that the call refuses.  plan: 4
+     values, or NULL: columns of a panel of B or Q in the workspace (0: operands
+     read in place), K ranges, stream-K tiles (of the first panel) and the
+     workspace bytes used. */
 int mcg_dense_path(int dtypeA, int layoutA, int layoutB, int64_t M, int64_t N, int64_t K, const void* A,
                    int64_t lda, const void* B, int64_t ldb);
 int mcg_dense_splits(int dtypeA, int layoutA, int layoutB, int64_t M, int64_t N, int64_t K, const void* A,
@@ -524,6 +532,10 @@ int mcg_dense_splits(int dtypeA, int layoutA, int layoutB, int64_t M, int64_t N,
                      double beta);
 int mcg_sparse24_path(int dtypeA, int layoutB, int64_t M, int64_t N, int64_t K, const void* A_compressed,
                       int64_t lda_c, const uint32_t* A_index, int64_t ld_idx, const void* B, int64_t ldb);
+int mcg_i8_scaled_path(int layoutB, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
+                       int64_t ldb, int64_t workspace_bytes, int64_t* plan);
+int mcg_grad_i8_path(int dtypeA, int layoutA, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
+                     const void* Q, int64_t ldq, int dtypeD, int64_t workspace_bytes, int64_t* plan);
 
 /*
  * mcg_mfma_eval -- one gfx950 matrix-core instruction per test vector, for

@@ -40,7 +40,7 @@ EXPORTS = ("gemm_dense", "gemm_dense_ws", "gemm_dense_noalloc", "mcg_dense_noall
            "mcg_mfma_probe",
            "rmsnorm_quant", "rmsnorm_backward", "mcg_rmsnorm_backward_workspace_bytes", "quantize_rows",
            "dequantize_rows", "gemm_i8_scaled", "mcg_i8_scaled_workspace_bytes", "gemm_grad_i8",
-           "mcg_grad_i8_workspace_bytes", "mcg_validate_rmsnorm_quant", "mcg_validate_rmsnorm_backward",
+           "mcg_grad_i8_workspace_bytes", "mcg_i8_scaled_path", "mcg_grad_i8_path", "mcg_validate_rmsnorm_quant", "mcg_validate_rmsnorm_backward",
            "mcg_validate_quantize_rows", "mcg_validate_dequantize_rows", "mcg_validate_i8_scaled",
            "mcg_validate_grad_i8")
 
@@ -117,6 +117,8 @@ _lib.gemm_grad_i8.argtypes = [_i32, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64
 _lib.mcg_validate_grad_i8.argtypes = _lib.gemm_grad_i8.argtypes[:-1]
 _lib.mcg_grad_i8_workspace_bytes.argtypes = [_i32, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i32]
 _lib.mcg_grad_i8_workspace_bytes.restype = _i64
+_lib.mcg_i8_scaled_path.argtypes = [_i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp]
+_lib.mcg_grad_i8_path.argtypes = [_i32, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i32, _i64, _vp]
 
 
 def lib():
@@ -447,6 +449,18 @@ def i8_scaled_workspace_bytes(layoutB, M, N, K, A, lda, B, ldb) -> int:
     return _lib.mcg_i8_scaled_workspace_bytes(_lay(layoutB), M, N, K, _ptr(A), lda, _ptr(B), ldb)
 
 
+def _path(fn, *args):
+    plan = (_i64 * 4)()
+    kernel = fn(*args, plan)
+    return kernel, dict(zip(("panel", "ranges", "streamk_tiles", "workspace"), plan))
+
+
+def i8_scaled_path(layoutB, M, N, K, A, lda, B, ldb, workspace_bytes=0):
+    """The kernel gemm_i8_scaled runs with a workspace of that size (include/mcg.h) and
+    its plan: columns of a panel, K ranges, stream-K tiles and workspace bytes used."""
+    return _path(_lib.mcg_i8_scaled_path, _lay(layoutB), M, N, K, _ptr(A), lda, _ptr(B), ldb, workspace_bytes)
+
+
 def gemm_grad_i8(dtypeA, layoutA, M, N, K, A, lda, Q, ldq, scaleK, C, D, ldd, dtypeD, beta=0.0, workspace=None,
                  workspace_bytes=0, stream=None) -> None:
     """D = A . (scaleK[k] * Q[k]) + beta * C, A 16-bit and Q int8 rows: the weight
@@ -462,6 +476,12 @@ def grad_i8_workspace_bytes(dtypeA, layoutA, M, N, K, A, lda, Q, ldq, dtypeD) ->
     """Workspace bytes gemm_grad_i8 can use for these operands."""
     return _lib.mcg_grad_i8_workspace_bytes(_dt(dtypeA), _lay(layoutA), M, N, K, _ptr(A), lda, _ptr(Q), ldq,
                                             _dt(dtypeD))
+
+
+def grad_i8_path(dtypeA, layoutA, M, N, K, A, lda, Q, ldq, dtypeD, workspace_bytes=0):
+    """The kernel gemm_grad_i8 runs with a workspace of that size, and its plan (i8_scaled_path)."""
+    return _path(_lib.mcg_grad_i8_path, _dt(dtypeA), _lay(layoutA), M, N, K, _ptr(A), lda, _ptr(Q), ldq, _dt(dtypeD),
+                 workspace_bytes)
 
 
 def validate_rmsnorm_quant(dtype, M, N, X, ldx, R, ldr, weight, eps, H, ldh, Q, ldq, scale, rstd=None) -> int:

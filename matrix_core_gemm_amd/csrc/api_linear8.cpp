@@ -245,6 +245,20 @@ int64_t mcg_i8_scaled_workspace_bytes(int layoutB, int64_t M, int64_t N, int64_t
   return mcg::plan_scaled(a, layoutB, current_num_cu(), INT64_MAX);
 }
 
+int mcg_i8_scaled_path(int layoutB, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
+                       int64_t ldb, int64_t workspace_bytes, int64_t* plan) {
+  if (!valid_layout(layoutB) || M <= 0 || N <= 0 || K < 0 || !sizes_ok(M, N) || K > 131071) return -1;
+  mcg::ScaledArgs a = scaled_args(M, N, K, A, lda, B, ldb, N, MCG_F32, nullptr);
+  const int64_t used = mcg::plan_scaled(a, layoutB, current_num_cu(), workspace_bytes);
+  if (plan) {
+    plan[0] = a.panel_n;
+    plan[1] = a.splits;
+    plan[2] = a.sk_tiles;
+    plan[3] = used;
+  }
+  return a.kernel == mcg::KERNEL_FAST ? mcg::pipe_kernel(a.tile) : a.kernel;
+}
+
 int gemm_i8_scaled(int layoutB, int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const float* scaleA,
                    const int8_t* B, int64_t ldb, const float* scaleB, const float* bias, void* D, int64_t ldd,
                    int dtypeD, void* workspace, int64_t workspace_bytes, void* stream) {
@@ -289,6 +303,23 @@ int64_t mcg_grad_i8_workspace_bytes(int dtypeA, int layoutA, int64_t M, int64_t 
     return 0;
   mcg::GradArgs a = grad_args(M, N, K, A, lda, Q, ldq, nullptr, nullptr, N, dtypeD, 0.0);
   return mcg::plan_grad(dtypeA, layoutA, a, current_num_cu(), INT64_MAX);
+}
+
+int mcg_grad_i8_path(int dtypeA, int layoutA, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
+                     const void* Q, int64_t ldq, int dtypeD, int64_t workspace_bytes, int64_t* plan) {
+  if ((dtypeA != MCG_BF16 && dtypeA != MCG_F16) || (dtypeD != dtypeA && dtypeD != MCG_F32) ||
+      !valid_layout(layoutA) || M <= 0 || N <= 0 || K < 0 || !sizes_ok(M, N) || !sizes_ok(K, 0))
+    return -1;
+  mcg::GradArgs a = grad_args(M, N, K, A, lda, Q, ldq, nullptr, nullptr, N, dtypeD, 0.0);
+  const int64_t used = mcg::plan_grad(dtypeA, layoutA, a, current_num_cu(), workspace_bytes);
+  const bool panels = a.panel_n > 0;
+  if (plan) {
+    plan[0] = a.panel_n;
+    plan[1] = panels ? 1 : a.splits;
+    plan[2] = panels ? a.sk_tiles : 0;
+    plan[3] = used;
+  }
+  return a.tiny ? mcg::KERNEL_TINY : panels ? mcg::pipe_kernel(a.pipe_tile) : mcg::KERNEL_GENERAL;
 }
 
 int gemm_grad_i8(int dtypeA, int layoutA, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,

@@ -304,7 +304,11 @@ double plan_panels(int dtA, int la, GradArgs& a, int num_cu, int64_t ws_bytes, i
   const int64_t panels = fixed + two * panel_bytes(a);
   DenseArgs d = dense_args(la, a, a.panel_n);
   const PipePlan pp = plan_pipe(dtA, d, num_cu, ws_bytes - panels);
-  *used = panels + pp.ws;
+  a.pipe_tile = pp.tile;
+  a.sk_tiles = d.sk_tiles;
+  // the last panel is narrower, and may take a stream-K split where the others do not
+  DenseArgs last = dense_args(la, a, a.N - (cdiv(a.N, a.panel_n) - 1) * a.panel_n);
+  *used = panels + std::max(pp.ws, plan_pipe(dtA, last, num_cu, ws_bytes - panels).ws);
   const double widen = pass_us((double)a.ka * a.ldw * (1 + 2 * two));
   return (fixed > 0 ? pass_us(2.0 * fixed) : 0.0) + cdiv(a.N, a.panel_n) * (widen + two * pp.us);
 }

@@ -193,7 +193,12 @@ double plan_panels(int lb, ScaledArgs& a, int num_cu, int64_t ws_bytes, int64_t*
   const int64_t bytes = fixed + panel_bytes(lb, a);
   ScaledArgs d = panel_args(lb, a, 0, a.panel_n);
   const PipePlan pp = plan_pipe(DT_I8, d, num_cu, ws_bytes - bytes);
-  *used = bytes + pp.ws;
+  a.kernel = KERNEL_FAST;
+  a.tile = pp.tile;
+  a.sk_tiles = d.sk_tiles;
+  // the last panel is narrower, and may take a stream-K split where the others do not
+  ScaledArgs last = panel_args(lb, a, 0, a.N - (cdiv(a.N, a.panel_n) - 1) * a.panel_n);
+  *used = bytes + std::max(pp.ws, plan_pipe(DT_I8, last, num_cu, ws_bytes - bytes).ws);
   constexpr double BYTE_US = 1 / 4.5e6, LAUNCH_US = 4.0;  // of the copies
   return 2.0 * fixed * BYTE_US + cdiv(a.N, a.panel_n) * (2.0 * panel_bytes(lb, a) * BYTE_US + LAUNCH_US + pp.us);
 }

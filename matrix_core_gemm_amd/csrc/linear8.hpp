@@ -63,7 +63,9 @@ struct ScaledArgs : DenseArgs {
   int64_t panel_n, kp, ldb2;
   int64_t ws_bytes;
 };
-constexpr int KERNEL_TINY = 16;  // (beside the dense kernels' codes)
+constexpr int KERNEL_HALF = 7, KERNEL_TINY = 16;  // (beside the dense kernels' codes; mcg_i8_scaled_path)
+// Code of the pipelined kernel with this tile.
+inline int pipe_kernel(int tile) { return tile == 256 ? KERNEL_FAST : tile == 128 ? KERNEL_MID : KERNEL_HALF; }
 int64_t plan_scaled(ScaledArgs& a, int layoutB, int num_cu, int64_t ws_bytes);
 hipError_t launch_scaled(int layoutB, const ScaledArgs& a, int num_cu, hipStream_t s);
 // The pipelined kernel with tile x tile tiles (256 or 128) and the streaming kernel (M <= 32).
@@ -94,6 +96,7 @@ struct GradArgs {
   int64_t ldw;         // of a panel, elements
   int64_t ka;          // K of the dense product: K, or a multiple of 8 with zeros past K
   int64_t lda2;        // of the copy of A, or 0: A is read in place
+  int pipe_tile, sk_tiles;  // of the first panel's product (each panel's is planned at its launch)
   void* ws;
   int64_t ws_bytes;
 };
