@@ -2,6 +2,9 @@
 takes (mcg_i8_scaled_path, mcg_grad_i8_path)."""
 import pytest
 
+import linear8_cases as cases
+import linear8_ref as ref
+
 m = pytest.importorskip("matrix_core_gemm_amd")
 
 BASE = 0x10000  # aligned and non-null; never dereferenced here
@@ -68,3 +71,38 @@ def test_paths_of_refused_and_empty_products():
     assert m.grad_i8_path("bf16", "k_contig", 8, 8, -1, BASE, 8, BASE, 8, "f32", FREE)[0] == -1
     assert m.grad_i8_path("bf16", "k_contig", 1, 1, 1, BASE, 1, BASE, 1, "f32", FREE)[0] == TINY
     assert m.grad_i8_path("bf16", "k_contig", 1, 1000, 500, BASE, 500, BASE, 1000, "bf16", 0)[0] == GENERAL
+
+
+@pytest.mark.parametrize("case", cases.SCALED, ids=str)
+def test_scaled_cases_plan_the_forms_they_are_for(case):
+    layout, M, N, K, aligned, ws, kernel, panels, streamk, ranges = case
+    lda, ldb = cases.scaled_lds(layout, M, N, K, aligned)
+    got, p = m.i8_scaled_path(layout, M, N, K, BASE, lda, BASE, ldb, ws)
+    assert (got, -(-N // p["panel"]) if p["panel"] else 0, p["streamk_tiles"], p["ranges"]) == (kernel, panels, streamk, ranges), p
+    assert panels < 2 or N % p["panel"]  # a last panel of its own width
+
+
+@pytest.mark.parametrize("dtA", ["bf16", "f16"])
+@pytest.mark.parametrize("case", cases.GRAD, ids=str)
+def test_gradient_cases_plan_the_forms_they_are_for(case, dtA):
+    dtD, layout, M, N, K, aligned, ws, kernel, panels, streamk = case
+    got, p = m.grad_i8_path(dtA, layout, M, N, K, BASE, cases.grad_lda(layout, M, K, aligned), BASE, N, "f32" if dtD == "f32" else dtA, ws)
+    assert (got, -(-N // p["panel"]) if p["panel"] else 0, p["streamk_tiles"]) == (kernel, panels, streamk), p
+    assert panels < 2 or N % p["panel"]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_the_bound_for_few_nonzeros_tells_a_missing_rest(dt):
+    # the kernels' two values in binary64: within the bound; without the rest far outside
+    M, N, K, n = 40, 60, 4096, 4
+    a = cases.few_nonzeros(1, M, K, n, dt)
+    q, s = cases.grad_inputs(2, K, N)
+    d, mag = ref.grad_i8(a, q, s, None, 0.0)
+    tol = cases.sparse_grad_tol(dt, a, d, mag, n)
+    hi, lo = cases.split_values(q, s, dt)
+    A = a.double()
+    assert bool(((A @ (hi + lo) - d).abs() <= tol).all())
+    bad = (A @ hi - d).abs() / tol
+    assert float(bad.max()) > 20 and float((bad > 1).double().mean()) > 0.9, bad.max()
+    for wrong in (A @ (hi - lo), A @ (hi + lo.roll(1, 1)), A @ (hi + lo.roll(1, 0))):  # a sign, a column or a row off
+        assert float((wrong - d).abs().div(tol).max()) > 20
