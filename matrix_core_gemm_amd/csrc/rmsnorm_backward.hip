@@ -7,7 +7,8 @@
 //
 // x comes in the type of dy or as an 8-bit checkpoint (codes and one scale per row).
 //
-// A row's threads hold it in registers between the sum and dx.  dw is a sum over
+// A row's threads hold it in registers between the sum and dx (rows of 8 to 8192
+// columns; others are read again).  dw is a sum over
 // rows: each workgroup walks rows a fixed stride apart, adds its threads' columns
 // in registers, and leaves one partial row in the workspace; a second kernel adds
 // the partial rows in a fixed order (no atomics: the result does not depend on
@@ -15,7 +16,9 @@
 //
 // Bound: memory (8 bytes per element with 16-bit x and dr).  8192 x 4096 bf16: 55 us
 // (4.9 TB/s), of which the sum of the partial rows takes 4; with 1024 partial rows,
-// summed by 8 threads a column one element at a time, and no loads ahead 87 us.
+// summed by 8 threads a column one element at a time, and no loads ahead 87 us.  Rows
+// above 8192 columns read x and dy twice for dx and once for dw: 8192 x 16384 bf16 329
+// us, 3.3 TB/s of the bytes that it cannot do without.
 #include "row_vec.hpp"
 
 namespace mcg {
@@ -171,7 +174,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(NormGr
   for (int v = 0; v < NV; ++v) store_vec<DT_F32>(part, at[v], narrow8<DT_F32>(dw[v]));
 }
 
-// Rows of any other length: dx with the row read twice, and dw's partial rows column by
+// Rows of any other length (above 8192, or under a vector): dx with the row read twice, and dw's partial rows column by
 // column (blockIdx.y is the part, threads along the columns).
 template <int DT, int DTX>
 __global__ __launch_bounds__(1024) void norm_grad_long_kernel(NormGradArgs p) {
@@ -274,7 +277,8 @@ static hipError_t launch_dt(const NormGradArgs& a, hipStream_t s) {
     // (as one of 8192, 4999 columns took 89 us instead of 86 for 8000 rows)
     else if (n >= 8 && n <= 6144) launch_one<DT, DTX, 384, 2>(a, s);
     else if (n >= 8 && n <= 8192) launch_one<DT, DTX, 512, 2>(a, s);
-    else if (n >= 8 && n <= 16384) launch_one<DT, DTX, 1024, 2>(a, s);
+    // (two vectors in each of 1024 threads, which have 128 registers, spilled 110 to 157
+    // of them: bf16 1 x 8200 40 us, 8192 x 12288 1089, 8192 x 16384 1143; so 9, 244 and 329)
     else {
       if (a.dW) {  // first: dX may be the memory of dY
         const dim3 grid((unsigned)((n + 2047) / 2048), (unsigned)a.parts);

@@ -1,5 +1,6 @@
-"""Registers of the stream-K kernels: the epilogue they share with the product with
-scales must not make an instance spill more than it did without it."""
+"""Registers: the stream-K kernels' epilogue, which they share with the product with
+scales, must not make an instance spill more than it did without it, and the row kernels
+must keep what they hold in registers there."""
 import os
 import re
 import shutil
@@ -12,23 +13,23 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 CSRC = os.path.join(ROOT, "matrix_core_gemm_amd", "csrc")
 
 
+def spills(tmp_path, src):
+    """Vector registers that each kernel of a source spills, compiled as build.py does."""
+    p = subprocess.run([HIPCC, "-x", "hip", "-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950", "-Xclang", "-target-feature",
+                        "-Xclang", "-packed-fp32-ops", "--cuda-device-only", "-Rpass-analysis=kernel-resource-usage", "-I" + CSRC,
+                        "-c", str(src), "-o", str(tmp_path / "source.o")], capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0, p.stderr
+    return {block.split()[0]: int(re.search(r"VGPRs Spill: (\d+)", block)[1]) for block in p.stderr.split("Function Name: ")[1:]}
+
+
 def spilled(tmp_path, op, args, la, lb):
-    """Vector registers that the 256 x 256 stream-K instance of gemm_fast_kernel spills."""
+    """Of the 256 x 256 stream-K instance of gemm_fast_kernel."""
     src = tmp_path / "instance.hip"
     src.write_text(f'#include "gemm_fast_kernel.hpp"\nnamespace mcg {{\nhipError_t instance(const {args}& a, hipStream_t s) '
                    f"{{ return fast::launch_one<fast::{op}, {la}, {lb}, 256, true>(a, s); }}\n}}\n")
-    # (as build.py compiles them)
-    p = subprocess.run([HIPCC, "-x", "hip", "-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950", "-Xclang", "-target-feature",
-                        "-Xclang", "-packed-fp32-ops", "--cuda-device-only", "-Rpass-analysis=kernel-resource-usage", "-I" + CSRC,
-                        "-c", str(src), "-o", str(tmp_path / "instance.o")], capture_output=True, text=True, timeout=300)
-    assert p.returncode == 0, p.stderr
-    found = {}
-    for block in p.stderr.split("Function Name: ")[1:]:
-        name = block.split()[0]
-        if "gemm_fast_kernel" in name and "Li256ELb1E" in name:
-            found[name] = int(re.search(r"VGPRs Spill: (\d+)", block)[1])
+    found = [n for name, n in spills(tmp_path, src).items() if "gemm_fast_kernel" in name and "Li256ELb1E" in name]
     assert len(found) == 1, found
-    return found.popitem()[1]
+    return found[0]
 
 
 @pytest.mark.skipif(shutil.which(HIPCC) is None, reason="no hipcc")
@@ -39,3 +40,10 @@ def spilled(tmp_path, op, args, la, lb):
 ])
 def test_stream_k_instances_spill_no_more_than_they_did(tmp_path, op, args, la, lb, most):
     assert spilled(tmp_path, op, args, la, lb) <= most
+
+
+@pytest.mark.skipif(shutil.which(HIPCC) is None, reason="no hipcc")
+@pytest.mark.parametrize("source", ["rows_quant.hip", "rmsnorm_backward.hip"])
+def test_row_kernels_spill_nothing(tmp_path, source):
+    found = spills(tmp_path, os.path.join(CSRC, source))
+    assert len(found) > 10 and not any(found.values()), {k: n for k, n in found.items() if n}
