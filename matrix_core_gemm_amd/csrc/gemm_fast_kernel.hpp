@@ -44,7 +44,9 @@
 //     of the 8-bit linear layer; gemm_fast_half.hip.)  The host takes it for problems with too few 256 x 256
 //     tiles when its cost model puts it ahead of the general kernel.
 // Preconditions (checked on the host): 16-byte aligned operands, K * elem_bytes
-// and ld * elem_bytes multiples of 16, M, N >= the tile size, and each workgroup's
+// and ld * elem_bytes multiples of 16 (gemm_dense also keeps M, N >= the tile size;
+// the 8-bit layer's plans send smaller ones, whose missing rows and columns lie
+// outside the buffer windows or are not stored), and each workgroup's
 // operand window below 2 GiB (32-bit buffer offsets).
 #pragma once
 #include "fast_tiles.hpp"

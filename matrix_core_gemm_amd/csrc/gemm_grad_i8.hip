@@ -315,11 +315,12 @@ double plan_panels(int dtA, int la, GradArgs& a, int num_cu, int64_t ws_bytes, i
 }  // namespace
 
 // Two ways: the general kernel widens Q's tiles on their way to LDS, once for every
-// 128 rows of A, and takes any operands; panels widen Q once into the workspace (a
-// copy's time for 3 or 5 bytes an element) and multiply on the pipelined dense
-// kernels, at about half the time per product.  The modelled times decide (bf16, in
-// place against panels: 64 x 4096 x 4096 21.2 and 33.5 us, 100 x 4096 x 4096 28.1 and
-// 31.4; 512^3 20.2 and 10.7, 4096^3 203 and 125, 8192^3 1480 and 873).
+// 128 rows of A, and takes any operands; panels widen Q once into the workspace (3 or
+// 5 bytes an element: 8192 x 4096 bf16 in 23 us, 4.3 TB/s; 4000 x 2048 f16 in 11, half
+// that rate) and multiply on the pipelined dense kernels, at about half the time per
+// product.  The modelled times decide (bf16, in place against panels: 64 x 4096 x 4096
+// 21.2 and 33.5 us, 100 x 4096 x 4096 28.1 and 31.4; 512^3 20.2 and 10.7, 4096^3 203 and
+// 125, 8192^3 1480 and 873).
 int64_t plan_grad(int dtA, int la, GradArgs& a, int num_cu, int64_t ws_bytes) {
   const int64_t nk = cdiv(a.K, KT_BYTES / 2);
   a.tile = general_rows(a.M);

@@ -14,6 +14,11 @@ int64_t cdiv(int64_t x, int64_t y) { return (x + y - 1) / y; }
 // epilogue (from 500 x 4096 x 4096 to 8192^3); stream-K's last round adds FIXUP_US and
 // a trip of its slots through the workspace.  16-bit 5703 x 1344 x 4288: 138 tiles of
 // 256 x 256 take 140 us, 495 of 128 x 128 85; int8 5536 x 768 x 832: 66 take 27, 264 20.
+// One set serves int8 and 16-bit operands in either order: over 48 to 8192 rows, five
+// N x K from 1024 x 4096 to 8192 x 8192 and five products (int8 in both orders, bf16 in
+// both, a binary32 result), 175 problems with each form forced, the choice is on geometric
+// mean 0.0 to 1.1% slower than the best and in three problems more than 10% (worst: binary32
+// result 704 x 2048 x 8192, 118 us with the general kernel, 101 with stream-K).
 struct TileTime {
   double kt_us, round_us;
 };

@@ -3,8 +3,8 @@
 //
 // The tiles have the LDS layout of tile_io.hpp (TileGeom, swz), so its fragment
 // readers apply.  gfx950 reads global memory at any byte address, so a chunk that
-// lies inside the matrix is one 16-byte load at any alignment; only the chunks
-// that cross the matrix's end are read by element.
+// lies inside the matrix is one 16-byte load at any alignment; a chunk that crosses
+// a row's end is read as the row's last 16 bytes and shifted.
 #pragma once
 #include "tile_io.hpp"
 
