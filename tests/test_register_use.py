@@ -1,6 +1,7 @@
 """Registers: the stream-K kernels' epilogue, which they share with the product with
-scales, must not make an instance spill more than it did without it, and the row kernels
-must keep what they hold in registers there."""
+scales, must not make an instance spill more than it did without it; nor may the dense
+streaming kernels change for theirs; and the row kernels must keep what they hold in
+registers there."""
 import os
 import re
 import shutil
@@ -13,13 +14,18 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 CSRC = os.path.join(ROOT, "matrix_core_gemm_amd", "csrc")
 
 
-def spills(tmp_path, src):
-    """Vector registers that each kernel of a source spills, compiled as build.py does."""
+def usage(tmp_path, src, what):
+    """A figure of each kernel of a source, compiled as build.py does."""
     p = subprocess.run([HIPCC, "-x", "hip", "-O3", "-std=c++17", "-fPIC", "--offload-arch=gfx950", "-Xclang", "-target-feature",
                         "-Xclang", "-packed-fp32-ops", "--cuda-device-only", "-Rpass-analysis=kernel-resource-usage", "-I" + CSRC,
                         "-c", str(src), "-o", str(tmp_path / "source.o")], capture_output=True, text=True, timeout=300)
     assert p.returncode == 0, p.stderr
-    return {block.split()[0]: int(re.search(r"VGPRs Spill: (\d+)", block)[1]) for block in p.stderr.split("Function Name: ")[1:]}
+    return {block.split()[0]: int(re.search(what + r": (\d+)", block)[1]) for block in p.stderr.split("Function Name: ")[1:]}
+
+
+def spills(tmp_path, src):
+    """Vector registers that each kernel of a source spills."""
+    return usage(tmp_path, src, "VGPRs Spill")
 
 
 def spilled(tmp_path, op, args, la, lb):
@@ -47,3 +53,18 @@ def test_stream_k_instances_spill_no_more_than_they_did(tmp_path, op, args, la, 
 def test_row_kernels_spill_nothing(tmp_path, source):
     found = spills(tmp_path, os.path.join(CSRC, source))
     assert len(found) > 10 and not any(found.values()), {k: n for k, n in found.items() if n}
+
+
+@pytest.mark.skipif(shutil.which(HIPCC) is None, reason="no hipcc")
+@pytest.mark.parametrize("op,la,lb,bw,most", [("BF16", "LAYOUT_K", "LAYOUT_K", 64, 42), ("I8", "LAYOUT_K", "LAYOUT_MN", 64, 42),
+                                              ("BF16", "LAYOUT_MN", "LAYOUT_MN", 64, 41)])
+def test_dense_streaming_instances_are_not_changed_by_the_product_with_scales(tmp_path, op, la, lb, bw, most):
+    # the loop that both once shared took two registers and an instruction more in the
+    # dense kernels (4 to 5% of their time)
+    with open(os.path.join(CSRC, "gemm_stream.hip")) as f:
+        source = f.read()
+    end = source.rindex("template <class Op, int LA, int LB, bool WIDE_A>\nstatic hipError_t launch_one")
+    src = tmp_path / "instance.hip"
+    src.write_text(source[:end] + f"template __global__ void gemm_stream_kernel<{op}, {la}, {lb}, false, {bw}>(DenseArgs);\n}}\n}}\n")
+    found = usage(tmp_path, src, r"\bVGPRs")
+    assert len(found) == 1 and max(found.values()) <= most, found
