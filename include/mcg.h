@@ -361,11 +361,11 @@ int decompress24_host(int dtype, int64_t M, int64_t K, const void* A_compressed,
  * Squares and sums are binary32, taken of the sum h before it is rounded.  The
  * quotient 127 y / max|y| is rounded to binary32 before it is to an integer, and
  * formed of binary32 values h * weight (rstd cancels): of 16-bit X without R and
- * weight the codes are those of the exact quotient, else of one within 2^-21 of
- * it (relative).  A row
- * whose y is all zero has scale 0.  A row with a NaN or an infinity, whose squares
- * or products h * weight overflow, or (possible with an eps below it only) whose
- * mean(h^2) + eps is under 2^-126, has scale NaN and codes 0.  N == 0 gives scale 0.
+ * weight the codes are those of the exact quotient, else of one within 2^-21 of it
+ * (relative).  A row whose y is all zero has scale 0.  A row with a NaN or an
+ * infinity, whose squares or products h * weight overflow, or (possible with an eps
+ * below it only) whose mean(h^2) + eps is under 2^-126, has scale NaN and codes 0.
+ * N == 0 gives scale 0.
  */
 int rmsnorm_quant(int dtype, int64_t M, int64_t N, const void* X, int64_t ldx, const void* R, int64_t ldr,
                   const void* weight, double eps, void* H, int64_t ldh, int8_t* Q, int64_t ldq, float* scale,
