@@ -5,8 +5,8 @@ argument order, turns torch tensors into device pointers, defaults the stream
 to torch's current stream, and raises ``MCGError`` on a non-zero status.  All
 arithmetic runs in the HIP kernels of ``_libmcg.so``; there is no fallback.
 If the library has not been built, importing this package fails.  The entry points
-of the 8-bit linear layer are called through a C extension (csrc/pycall.c) where it
-is built for this Python, else through ctypes like the others.
+of the 8-bit linear layer and of the products by group are called through a C extension
+(csrc/pycall.c) where it is built for this Python, else through ctypes like the others.
 
 dtype and layout arguments take the C enum values or their names:
   dtypes : "bf16", "f16", "i8", "e4m3", "e5m2", "f32", "i32", "f64"
@@ -42,7 +42,11 @@ EXPORTS = ("gemm_dense", "gemm_dense_ws", "gemm_dense_noalloc", "mcg_dense_noall
            "dequantize_rows", "gemm_i8_scaled", "mcg_i8_scaled_workspace_bytes", "gemm_grad_i8",
            "mcg_grad_i8_workspace_bytes", "mcg_i8_scaled_path", "mcg_grad_i8_path", "mcg_validate_rmsnorm_quant", "mcg_validate_rmsnorm_backward",
            "mcg_validate_quantize_rows", "mcg_validate_dequantize_rows", "mcg_validate_i8_scaled",
-           "mcg_validate_grad_i8")
+           "mcg_validate_grad_i8",
+           "quantize_blocks", "dequantize_blocks", "gemm_f8_blocks", "gemm_grouped", "gemm_grouped_grad",
+           "gemm_grouped_f8_blocks", "mcg_grouped_path", "mcg_grouped_grad_path", "mcg_validate_quantize_blocks",
+           "mcg_validate_dequantize_blocks", "mcg_validate_f8_blocks", "mcg_validate_grouped",
+           "mcg_validate_grouped_grad", "mcg_validate_grouped_f8_blocks")
 
 
 class MCGError(RuntimeError):
@@ -119,6 +123,23 @@ _lib.mcg_grad_i8_workspace_bytes.argtypes = [_i32, _i32, _i64, _i64, _i64, _vp, 
 _lib.mcg_grad_i8_workspace_bytes.restype = _i64
 _lib.mcg_i8_scaled_path.argtypes = [_i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp]
 _lib.mcg_grad_i8_path.argtypes = [_i32, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i32, _i64, _vp]
+_lib.quantize_blocks.argtypes = [_i32, _i32, _i32, _i32, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp]
+_lib.mcg_validate_quantize_blocks.argtypes = _lib.quantize_blocks.argtypes[:-1]
+_lib.dequantize_blocks.argtypes = [_i32, _i32, _i32, _i32, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp]
+_lib.mcg_validate_dequantize_blocks.argtypes = _lib.dequantize_blocks.argtypes[:-1]
+_lib.gemm_f8_blocks.argtypes = [_i32, _i32, _i32, _i32, _i32, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
+                                _vp, _vp, _i64, _i32, _dbl, _vp]
+_lib.mcg_validate_f8_blocks.argtypes = _lib.gemm_f8_blocks.argtypes[:-1]
+_lib.gemm_grouped.argtypes = [_i32, _i32, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i32, _vp]
+_lib.mcg_validate_grouped.argtypes = _lib.gemm_grouped.argtypes[:-1]
+_lib.gemm_grouped_grad.argtypes = [_i32, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i64, _i32, _dbl,
+                                   _vp]
+_lib.mcg_validate_grouped_grad.argtypes = _lib.gemm_grouped_grad.argtypes[:-1]
+_lib.gemm_grouped_f8_blocks.argtypes = [_i32, _i32, _i32, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _i64,
+                                        _vp, _i64, _i64, _vp, _i64, _i32, _vp]
+_lib.mcg_validate_grouped_f8_blocks.argtypes = _lib.gemm_grouped_f8_blocks.argtypes[:-1]
+_lib.mcg_grouped_path.argtypes = [_i32, _i32, _i32, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _i32, _i32, _vp]
+_lib.mcg_grouped_grad_path.argtypes = [_i32, _i64, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i32, _vp]
 
 
 def lib():
@@ -175,10 +196,14 @@ def _check(fn: str, status: int) -> None:
 class _CtypesCalls:
     """csrc/pycall.c's calls through ctypes: positional arguments in the C order, the
     stream last, converted by kind -- d dtype, l layout, i integer, f float, p device
-    address, b bytes of the workspace before it, s stream.  Returns the status."""
+    address, b bytes of the workspace before it, k a block's extent, s stream.  Returns the
+    status."""
 
     KINDS = {"rmsnorm_quant": "diipipipfpipipps", "rmsnorm_backward": "ddiipipippppipippbs", "quantize_rows": "diipipips",
-             "dequantize_rows": "diipippis", "gemm_i8_scaled": "liiipippipppidpbs", "gemm_grad_i8": "dliiipipipppidfpbs"}
+             "dequantize_rows": "diipippis", "gemm_i8_scaled": "liiipippipppidpbs", "gemm_grad_i8": "dliiipipipppidfpbs",
+             "quantize_blocks": "ddkkiipipipis", "dequantize_blocks": "ddkkiipipipis",
+             "gemm_f8_blocks": "ddllkiiipipipipippidfs", "gemm_grouped": "dliiiippipiipids",
+             "gemm_grouped_grad": "diiiippipippiidfs", "gemm_grouped_f8_blocks": "ddliiiippipipiipiipids"}
 
     def __getattr__(self, name):
         kinds, fn = self.KINDS[name], getattr(_lib, name)
@@ -195,6 +220,10 @@ class _CtypesCalls:
         if not -1 << 63 <= v < 1 << 63:
             raise OverflowError("integer too large for 64 bits")
         return v
+
+    def _k(self, v, _):
+        v = self._i(v)
+        return v if v in (1, 128) else 0  # (a C int: no longer integer wraps into one)
 
     def _d(self, v, _):
         return DTYPES[v] if isinstance(v, str) else self._i(v)
@@ -484,6 +513,73 @@ def grad_i8_path(dtypeA, layoutA, M, N, K, A, lda, Q, ldq, dtypeD, workspace_byt
                  workspace_bytes)
 
 
+def quantize_blocks(dtype, dtypeQ, blockM, blockN, M, N, X, ldx, Q, ldq, scale, lds, stream=None) -> None:
+    """X in 8-bit floats with a scale for each block (1 x 128, 128 x 1 or 128 x 128)."""
+    status = _mcgcall.quantize_blocks(dtype, dtypeQ, blockM, blockN, M, N, X, ldx, Q, ldq, scale, lds, stream)
+    if status:
+        raise MCGError("quantize_blocks", status)
+
+
+def dequantize_blocks(dtypeQ, dtypeD, blockM, blockN, M, N, Q, ldq, scale, lds, D, ldd, stream=None) -> None:
+    """The values of block-scaled codes, rounded once to dtypeD."""
+    status = _mcgcall.dequantize_blocks(dtypeQ, dtypeD, blockM, blockN, M, N, Q, ldq, scale, lds, D, ldd, stream)
+    if status:
+        raise MCGError("dequantize_blocks", status)
+
+
+def gemm_f8_blocks(dtypeA, dtypeB, layoutA, layoutB, blockB, M, N, K, A, lda, scaleA, ldsa, B, ldb, scaleB, ldsb, C, D,
+                   ldd, dtypeD, beta=0.0, stream=None) -> None:
+    """D = A . B + beta * C on 8-bit floats whose blocks of 128 k carry a scale each: per row
+    of A, and per blockB (1 or 128) columns of B."""
+    status = _mcgcall.gemm_f8_blocks(dtypeA, dtypeB, layoutA, layoutB, blockB, M, N, K, A, lda, scaleA, ldsa, B, ldb,
+                                     scaleB, ldsb, C, D, ldd, dtypeD, beta, stream)
+    if status:
+        raise MCGError("gemm_f8_blocks", status)
+
+
+def gemm_grouped(dtype, layoutB, G, M, N, K, offsets, A, lda, B, ldb, strideB, D, ldd, dtypeD, stream=None) -> None:
+    """D[r] = A[r] . B_g for the rows r of each group g: offsets[g] .. offsets[g + 1] - 1
+    (G + 1 int32 values on the device).  Other rows of D are left as they were."""
+    status = _mcgcall.gemm_grouped(dtype, layoutB, G, M, N, K, offsets, A, lda, B, ldb, strideB, D, ldd, dtypeD, stream)
+    if status:
+        raise MCGError("gemm_grouped", status)
+
+
+def gemm_grouped_grad(dtype, G, M, N, K, offsets, A, lda, B, ldb, C, D, ldd, strideD, dtypeD, beta=0.0,
+                      stream=None) -> None:
+    """D_g = A_g^T . B_g + beta * C_g over the rows of each group: the weight gradients of
+    gemm_grouped (A = dY, B = x)."""
+    status = _mcgcall.gemm_grouped_grad(dtype, G, M, N, K, offsets, A, lda, B, ldb, C, D, ldd, strideD, dtypeD, beta,
+                                        stream)
+    if status:
+        raise MCGError("gemm_grouped_grad", status)
+
+
+def gemm_grouped_f8_blocks(dtypeA, dtypeB, layoutB, G, M, N, K, offsets, A, lda, scaleA, ldsa, B, ldb, strideB, scaleB,
+                           ldsb, strideSB, D, ldd, dtypeD, stream=None) -> None:
+    """gemm_grouped on block-scaled 8-bit floats (A 1 x 128, B 128 x 128)."""
+    status = _mcgcall.gemm_grouped_f8_blocks(dtypeA, dtypeB, layoutB, G, M, N, K, offsets, A, lda, scaleA, ldsa, B, ldb,
+                                             strideB, scaleB, ldsb, strideSB, D, ldd, dtypeD, stream)
+    if status:
+        raise MCGError("gemm_grouped_f8_blocks", status)
+
+
+def grouped_path(dtype, layoutA, layoutB, G, M, N, K, A, lda, B, ldb, strideB, blockB, dtypeD):
+    """The kernel (include/mcg.h) and rows of a tile of gemm_grouped and gemm_grouped_f8_blocks,
+    and with G = 0 of gemm_f8_blocks."""
+    plan = (_i64 * 1)()
+    kernel = _lib.mcg_grouped_path(_dt(dtype), _lay(layoutA), _lay(layoutB), G, M, N, K, _ptr(A), lda, _ptr(B), ldb,
+                                   strideB, blockB, _dt(dtypeD), plan)
+    return kernel, plan[0]
+
+
+def grouped_grad_path(dtype, G, M, N, K, A, lda, B, ldb, dtypeD):
+    """The kernel and rows of a tile of gemm_grouped_grad."""
+    plan = (_i64 * 1)()
+    kernel = _lib.mcg_grouped_grad_path(_dt(dtype), G, M, N, K, _ptr(A), lda, _ptr(B), ldb, _dt(dtypeD), plan)
+    return kernel, plan[0]
+
+
 def validate_rmsnorm_quant(dtype, M, N, X, ldx, R, ldr, weight, eps, H, ldh, Q, ldq, scale, rstd=None) -> int:
     return _lib.mcg_validate_rmsnorm_quant(_dt(dtype), M, N, _ptr(X), ldx, _ptr(R), ldr, _ptr(weight), float(eps),
                                            _ptr(H), ldh, _ptr(Q), ldq, _ptr(scale), _ptr(rstd))
@@ -517,3 +613,37 @@ def validate_grad_i8(dtypeA, layoutA, M, N, K, A, lda, Q, ldq, scaleK, C, D, ldd
     ws, nb = _workspace(workspace, workspace_bytes)
     return _lib.mcg_validate_grad_i8(_dt(dtypeA), _lay(layoutA), M, N, K, _ptr(A), lda, _ptr(Q), ldq, _ptr(scaleK),
                                      _ptr(C), _ptr(D), ldd, _dt(dtypeD), float(beta), ws, nb)
+
+
+def validate_quantize_blocks(dtype, dtypeQ, blockM, blockN, M, N, X, ldx, Q, ldq, scale, lds) -> int:
+    return _lib.mcg_validate_quantize_blocks(_dt(dtype), _dt(dtypeQ), blockM, blockN, M, N, _ptr(X), ldx, _ptr(Q), ldq,
+                                             _ptr(scale), lds)
+
+
+def validate_dequantize_blocks(dtypeQ, dtypeD, blockM, blockN, M, N, Q, ldq, scale, lds, D, ldd) -> int:
+    return _lib.mcg_validate_dequantize_blocks(_dt(dtypeQ), _dt(dtypeD), blockM, blockN, M, N, _ptr(Q), ldq,
+                                               _ptr(scale), lds, _ptr(D), ldd)
+
+
+def validate_f8_blocks(dtypeA, dtypeB, layoutA, layoutB, blockB, M, N, K, A, lda, scaleA, ldsa, B, ldb, scaleB, ldsb, C,
+                       D, ldd, dtypeD, beta=0.0) -> int:
+    return _lib.mcg_validate_f8_blocks(_dt(dtypeA), _dt(dtypeB), _lay(layoutA), _lay(layoutB), blockB, M, N, K, _ptr(A),
+                                       lda, _ptr(scaleA), ldsa, _ptr(B), ldb, _ptr(scaleB), ldsb, _ptr(C), _ptr(D), ldd,
+                                       _dt(dtypeD), float(beta))
+
+
+def validate_grouped(dtype, layoutB, G, M, N, K, offsets, A, lda, B, ldb, strideB, D, ldd, dtypeD) -> int:
+    return _lib.mcg_validate_grouped(_dt(dtype), _lay(layoutB), G, M, N, K, _ptr(offsets), _ptr(A), lda, _ptr(B), ldb,
+                                     strideB, _ptr(D), ldd, _dt(dtypeD))
+
+
+def validate_grouped_grad(dtype, G, M, N, K, offsets, A, lda, B, ldb, C, D, ldd, strideD, dtypeD, beta=0.0) -> int:
+    return _lib.mcg_validate_grouped_grad(_dt(dtype), G, M, N, K, _ptr(offsets), _ptr(A), lda, _ptr(B), ldb, _ptr(C),
+                                          _ptr(D), ldd, strideD, _dt(dtypeD), float(beta))
+
+
+def validate_grouped_f8_blocks(dtypeA, dtypeB, layoutB, G, M, N, K, offsets, A, lda, scaleA, ldsa, B, ldb, strideB,
+                               scaleB, ldsb, strideSB, D, ldd, dtypeD) -> int:
+    return _lib.mcg_validate_grouped_f8_blocks(_dt(dtypeA), _dt(dtypeB), _lay(layoutB), G, M, N, K, _ptr(offsets),
+                                               _ptr(A), lda, _ptr(scaleA), ldsa, _ptr(B), ldb, strideB, _ptr(scaleB),
+                                               ldsb, strideSB, _ptr(D), ldd, _dt(dtypeD))

@@ -1,8 +1,9 @@
-/* pycall.c -- Python calls of the 8-bit linear layer's entry points (include/mcg.h)
- * without ctypes: the small operators take 2.7 us to launch, and marshalling a dozen
- * arguments through ctypes and Python took as long again.  Arguments come by position,
- * in the C order; a tensor gives its address, None a null pointer, an integer itself.
- * Each function returns the mcg_status; the stream's None is torch's current stream.
+/* pycall.c -- Python calls of the 8-bit linear layer's entry points and of the products
+ * by group (include/mcg.h) without ctypes: the small operators take 2.7 us to launch, and
+ * marshalling a dozen arguments through ctypes and Python took as long again.  Arguments
+ * come by position, in the C order; a tensor gives its address, None a null pointer, an
+ * integer itself.  Each function returns the mcg_status; the stream's None is torch's
+ * current stream.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -94,6 +95,8 @@ static int count_ok(const char *name, Py_ssize_t got, Py_ssize_t want) {
 #define PTR(i) void *const a##i = as_ptr(v[i])
 #define DT(i) const int a##i = as_enum(v[i], dtypes)
 #define LAY(i) const int a##i = as_enum(v[i], layouts)
+/* A block's extent as an int, which no long integer wraps into. */
+static int block(int64_t n) { return n == 1 || n == 128 ? (int)n : 0; }
 #define DBL(i) const double a##i = PyErr_Occurred() ? 0.0 : PyFloat_AsDouble(v[i])
 
 static PyObject *py_rmsnorm_quant(PyObject *self, PyObject *const *v, Py_ssize_t n) {
@@ -138,6 +141,48 @@ static PyObject *py_gemm_grad_i8(PyObject *self, PyObject *const *v, Py_ssize_t 
   CALL(gemm_grad_i8(a0, a1, a2, a3, a4, a5, a6, a7, a8, a9, a10, a11, a12, a13, a14, a15, bytes, stream));
 }
 
+static PyObject *py_quantize_blocks(PyObject *self, PyObject *const *v, Py_ssize_t n) {
+  if (!count_ok("quantize_blocks", n, 13)) return NULL;
+  DT(0); DT(1); INT(2); INT(3); INT(4); INT(5); PTR(6); INT(7); PTR(8); INT(9); PTR(10); INT(11);
+  void *const stream = as_stream(v[12]);
+  CALL(quantize_blocks(a0, a1, block(a2), block(a3), a4, a5, a6, a7, a8, a9, a10, a11, stream));
+}
+static PyObject *py_dequantize_blocks(PyObject *self, PyObject *const *v, Py_ssize_t n) {
+  if (!count_ok("dequantize_blocks", n, 13)) return NULL;
+  DT(0); DT(1); INT(2); INT(3); INT(4); INT(5); PTR(6); INT(7); PTR(8); INT(9); PTR(10); INT(11);
+  void *const stream = as_stream(v[12]);
+  CALL(dequantize_blocks(a0, a1, block(a2), block(a3), a4, a5, a6, a7, a8, a9, a10, a11, stream));
+}
+static PyObject *py_gemm_f8_blocks(PyObject *self, PyObject *const *v, Py_ssize_t n) {
+  if (!count_ok("gemm_f8_blocks", n, 22)) return NULL;
+  DT(0); DT(1); LAY(2); LAY(3); INT(4); INT(5); INT(6); INT(7); PTR(8); INT(9); PTR(10); INT(11); PTR(12); INT(13); PTR(14);
+  INT(15); PTR(16); PTR(17); INT(18); DT(19); DBL(20);
+  void *const stream = as_stream(v[21]);
+  CALL(gemm_f8_blocks(a0, a1, a2, a3, block(a4), a5, a6, a7, a8, a9, a10, a11, a12, a13, a14, a15, a16, a17, a18, a19, a20,
+                      stream));
+}
+static PyObject *py_gemm_grouped(PyObject *self, PyObject *const *v, Py_ssize_t n) {
+  if (!count_ok("gemm_grouped", n, 16)) return NULL;
+  DT(0); LAY(1); INT(2); INT(3); INT(4); INT(5); PTR(6); PTR(7); INT(8); PTR(9); INT(10); INT(11); PTR(12); INT(13); DT(14);
+  void *const stream = as_stream(v[15]);
+  CALL(gemm_grouped(a0, a1, a2, a3, a4, a5, a6, a7, a8, a9, a10, a11, a12, a13, a14, stream));
+}
+static PyObject *py_gemm_grouped_grad(PyObject *self, PyObject *const *v, Py_ssize_t n) {
+  if (!count_ok("gemm_grouped_grad", n, 17)) return NULL;
+  DT(0); INT(1); INT(2); INT(3); INT(4); PTR(5); PTR(6); INT(7); PTR(8); INT(9); PTR(10); PTR(11); INT(12); INT(13); DT(14);
+  DBL(15);
+  void *const stream = as_stream(v[16]);
+  CALL(gemm_grouped_grad(a0, a1, a2, a3, a4, a5, a6, a7, a8, a9, a10, a11, a12, a13, a14, a15, stream));
+}
+static PyObject *py_gemm_grouped_f8_blocks(PyObject *self, PyObject *const *v, Py_ssize_t n) {
+  if (!count_ok("gemm_grouped_f8_blocks", n, 22)) return NULL;
+  DT(0); DT(1); LAY(2); INT(3); INT(4); INT(5); INT(6); PTR(7); PTR(8); INT(9); PTR(10); INT(11); PTR(12); INT(13); INT(14);
+  PTR(15); INT(16); INT(17); PTR(18); INT(19); DT(20);
+  void *const stream = as_stream(v[21]);
+  CALL(gemm_grouped_f8_blocks(a0, a1, a2, a3, a4, a5, a6, a7, a8, a9, a10, a11, a12, a13, a14, a15, a16, a17, a18, a19, a20,
+                              stream));
+}
+
 /* setup(dtypes, layouts, to_stream, raw_stream, raw_device), once, by the package. */
 static PyObject *py_setup(PyObject *self, PyObject *args) {
   if (!PyArg_ParseTuple(args, "O!O!OOO", &PyDict_Type, &dtypes, &PyDict_Type, &layouts, &to_stream, &raw_stream, &raw_device))
@@ -152,7 +197,9 @@ static PyObject *py_setup(PyObject *self, PyObject *args) {
 
 #define ENTRY(f) {#f, (PyCFunction)(void (*)(void))py_##f, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {ENTRY(rmsnorm_quant), ENTRY(rmsnorm_backward), ENTRY(quantize_rows), ENTRY(dequantize_rows),
-                                ENTRY(gemm_i8_scaled), ENTRY(gemm_grad_i8), {"setup", py_setup, METH_VARARGS, NULL}, {NULL}};
+                                ENTRY(gemm_i8_scaled), ENTRY(gemm_grad_i8),
+                                ENTRY(quantize_blocks), ENTRY(dequantize_blocks), ENTRY(gemm_f8_blocks), ENTRY(gemm_grouped),
+                                ENTRY(gemm_grouped_grad), ENTRY(gemm_grouped_f8_blocks), {"setup", py_setup, METH_VARARGS, NULL}, {NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mcgcall", NULL, -1, methods};
 
 PyMODINIT_FUNC PyInit__mcgcall(void) {
