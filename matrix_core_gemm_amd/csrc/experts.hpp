@@ -55,6 +55,12 @@ struct BlocksArgs {
 hipError_t launch_blocks_quant(int dt, int dtQ, int bm, int bn, const BlocksArgs& a, hipStream_t s);
 hipError_t launch_blocks_dequant(int dtQ, int dt, int bm, int bn, const BlocksArgs& a, hipStream_t s);
 
+// The pipelined product of block-scaled 8-bit floats (f8_blocks_kernel.hpp), 256 x 256 and 128 x 128
+// tiles: A and B K-contiguous or B MN-contiguous with blockB 128, or both MN-contiguous with blockB 1.
+// wide: exact products (f16 and binary32 D).
+hipError_t launch_f8_blocks_256(int dtA, int la, int lb, int blockB, const GroupArgs& a, hipStream_t s);
+hipError_t launch_f8_blocks_128(int dtA, int la, int lb, int blockB, bool wide, const GroupArgs& a, hipStream_t s);
+
 // The choice of a kernel, and its launch (expert_plan.cpp).
 GroupPlan plan_grouped(int dt, int la, int lb, const GroupArgs& a, int num_cu);
 GroupPlan plan_grouped_grad(int dt, const GroupArgs& a, int num_cu);

@@ -1,0 +1,358 @@
+// f8_blocks_kernel.hpp -- the pipelined product of block-scaled 8-bit floats, for
+// operands with 16-byte rows, over all rows or by group:
+//
+//   D[i][j] = sum_b sa[i][b] sb[b][j] sum_{k in b} A[i][k] B[k][j] + beta C[i][j]
+//
+// The scales change with every block of 128 k, so a block's sum has to leave the matrix
+// instruction before it is scaled.  One 16 x 16 x 128 instruction is one block of a 16 x 16
+// tile, and its result four registers: p = A B (with no accumulator), then
+// acc += (sa sb) p on the vector unit, 4 fused steps of 4 cycles for an instruction of 32
+// cycles, which run beside the matrix core (the next row of instructions is
+// issued first).  With 32 x 32 x 64 instructions a block is a chain of two and its result 16
+// registers, which do not fit beside 128 accumulators and the fragments.
+//
+// Tile TB x TB by 8 (TB 256) or 4 (TB 128) wavefronts, each (TB / 2) x 64 outputs.  A K tile
+// is one block: 128 bytes of each row, in two LDS stages filled by buffer_load ... lds (16
+// bytes per lane), with its scales of the tile's rows and columns (one 4-byte load per lane).
+// A wavefront walks down its rows 16 by 16: the next 16 rows' fragment is read from LDS
+// while 4 instructions (64 columns, whose fragments stay in registers) run on this one.
+// The K tile's barrier stands two rows of instructions before its end, where the last
+// fragments are in registers: its stage is then free for the K tile after next, and the
+// instructions that are left cover the barrier and the DMA's issue.
+//
+// For D in bf16 the products run on the 8-bit instruction, which keeps about 13 bits below the
+// largest of 8 consecutive products: off by 2^-12 of D, typically, where bf16 rounds at
+// 2^-8.  For f16 and binary32 D the codes are widened exactly to bf16 (WIDE), four
+// instructions of 32 k for a block.
+#pragma once
+#include "fast_tiles.hpp"
+#include "group_epilogue.hpp"
+#include "group_tiles.hpp"
+
+namespace mcg {
+namespace f8b {
+
+using namespace fast;
+
+constexpr int KT = SCALE_BLOCK;  // k (and bytes) of a K tile
+
+// LDS rows of MN-contiguous tiles (one k each, TB bytes): 16-byte chunks are XOR-ed so that the
+// transposing reads of 16 columns, 8 k from each of two lane groups 16 k apart in a cycle, fall
+// in distinct banks.  The pattern repeats every 32 rows.
+template <int TB>
+__device__ __forceinline__ int mn_swz(int row) {
+  if constexpr (TB == 256) return (row & 7) | (8 * ((row >> 4) & 1));
+  else return ((row >> 1) & 3) | (4 * ((row >> 4) & 1));
+}
+
+// HBM -> LDS loader of one operand's K tiles: wavefront q of 4 writes LDS bytes
+// [(i * 4 + q) * 1024, +1024) in instruction i, INSTR instructions in all.
+template <int LAYOUT, int TB>
+struct TileDma {
+  static constexpr int INSTR = TB * KT / 4096;
+  LineLoader<1, LAYOUT_K, TB, KT> line;  // K-contiguous
+  __amdgpu_buffer_rsrc_t rsrc;           // MN-contiguous
+  uint32_t voff[2], istride, kstride;
+
+  // base: the operand's first row (or column) of the tile; rows of it that exist: mn
+  __device__ __forceinline__ void init(const char* base, int64_t ld, int64_t mn, int64_t x0, int64_t K, int q, int lane) {
+    if constexpr (LAYOUT == LAYOUT_K) {
+      line.init(base + x0 * ld, (uint32_t)(min(mn - x0, (int64_t)TB) * ld), ld, K, q, lane);
+    } else {
+      rsrc = make_rsrc(base + x0, mn_window(K, ld, mn, x0, 1));
+      constexpr int CPR = TB / 16, RPI = 256 / CPR;  // chunks per LDS row, rows per instruction
+      const int c = q * 64 + lane, r = c / CPR;
+      voff[0] = (uint32_t)(r * ld + 16 * ((c % CPR) ^ mn_swz<TB>(r)));
+      voff[1] = (uint32_t)(r * ld + 16 * ((c % CPR) ^ mn_swz<TB>(r + RPI)));
+      istride = __builtin_amdgcn_readfirstlane((uint32_t)(RPI * ld));
+      kstride = __builtin_amdgcn_readfirstlane((uint32_t)(KT * ld));
+    }
+  }
+  // instructions [i0, i0 + n) of K tile kt (past the end: zeros)
+  template <int N>
+  __device__ __forceinline__ void issue(lds_char* dst, int kt, int i0, int q) const {
+    if constexpr (LAYOUT == LAYOUT_K) {
+      line.issue(dst, kt, i0, N, q);
+    } else {
+#pragma unroll
+      for (int u = 0; u < N; ++u) {
+        const int i = i0 + u;
+        // (i0 is even: u tells which half of the pattern's 32 rows)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)(dst + (i * 4 + q) * 1024), 16,
+                                                 voff[TB == 256 ? u & 1 : 0] + (uint32_t)kt * kstride + (uint32_t)i * istride, 0, 0, 0);
+      }
+    }
+  }
+};
+
+// Fragments: 32 k of a row (or column) in each lane, lane group g = lane / 16 with k 16 g .. 16 g +
+// 15 and 64 + 16 g .. 64 + 16 g + 15 of the K tile.
+template <int LAYOUT, int TB, int N>
+__device__ __forceinline__ void read_frags(const lds_char* tile, int rb, int lane, i32x8 (&f)[N]) {
+  const int g = lane >> 4;
+  if constexpr (LAYOUT == LAYOUT_K) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int r = rb + 16 * n + (lane & 15), s = (r >> 1) & 7;
+      const i32x4 x = lds_read_b128(tile, r * KT + ((g ^ s) << 4)), y = lds_read_b128(tile, r * KT + (((g + 4) ^ s) << 4));
+      f[n] = i32x8{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    }
+  } else {
+    const int L = lane & 15, row = 16 * g + (L >> 1);
+    uint32_t ad[N];
+    i32x2 r[N][4];
+#pragma unroll
+    for (int n = 0; n < N; ++n) ad[n] = lds_addr(tile + row * TB + (((rb / 16 + n) ^ mn_swz<TB>(row)) << 4) + 8 * (L & 1));
+    lds_read_tr_x4<1, 8 * TB, 64 * TB, 72 * TB>(ad, r);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+      f[n] = i32x8{r[n][0].x, r[n][0].y, r[n][1].x, r[n][1].y, r[n][2].x, r[n][2].y, r[n][3].x, r[n][3].y};
+  }
+}
+
+// A block's product of 16 x 16 outputs.  FA: format of A; B is E4M3.
+template <int FA>
+struct Native {
+  using frag_t = i32x8;
+  static constexpr bool WIDE = false;
+  __device__ static __forceinline__ frag_t a(const i32x8& v) { return v; }
+  __device__ static __forceinline__ frag_t b(const i32x8& v) { return v; }
+  __device__ static __forceinline__ f32x4 block(const frag_t& fb, const frag_t& fa) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, fa, f32x4{0, 0, 0, 0}, 0, FA, 0, 0, 0, 0);
+  }
+};
+struct WideFrag {
+  i32x4 s[4];  // 8 bf16 values for each of 4 instructions
+};
+template <int FA>
+struct Wide {
+  using frag_t = WideFrag;
+  static constexpr bool WIDE = true;
+  template <int FMT>
+  __device__ static __forceinline__ frag_t widen(const i32x8& v) {
+    frag_t f;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        bf16x2 x;
+        if constexpr (FMT == 0) {
+          x = h & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * s + h / 2], 1.0f, true)
+                    : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[2 * s + h / 2], 1.0f, false);
+        } else {
+          x = h & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(v[2 * s + h / 2], 1.0f, true)
+                    : __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(v[2 * s + h / 2], 1.0f, false);
+        }
+        f.s[s][h] = bit_cast<int>(x);
+      }
+    }
+    return f;
+  }
+  __device__ static __forceinline__ frag_t a(const i32x8& v) { return widen<FA>(v); }
+  __device__ static __forceinline__ frag_t b(const i32x8& v) { return widen<0>(v); }
+  __device__ static __forceinline__ f32x4 block(const frag_t& fb, const frag_t& fa) {
+    f32x4 p = {0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bit_cast<bf16x8>(fb.s[s]), bit_cast<bf16x8>(fa.s[s]), p, 0, 0, 0);
+    return p;
+  }
+};
+
+// BLKB: columns of B under one scale (128 or 1).
+template <class Op, int LA, int LB, int BLKB, int TB>
+__global__ __launch_bounds__(2 * TB) __attribute__((amdgpu_waves_per_eu(2, 2))) void f8_blocks_kernel(GroupArgs p) {
+  constexpr int NWAVES = TB / 32, WN = TB / 64;  // wavefronts, 2 x WN of them
+  constexpr int WTM = TB / 32, WTN = 4;          // 16 x 16 blocks of a wavefront
+  constexpr int STAGE = TB * KT, SCALES = 2 * TB * 4;
+  using DmaA = TileDma<LA, TB>;
+  using DmaB = TileDma<LB, TB>;
+  constexpr int HALVES = NWAVES / 4, IA = DmaA::INSTR / HALVES;  // instructions per wavefront, operand and K tile
+  __shared__ __attribute__((aligned(1024))) char smem_raw[2 * (2 * STAGE + SCALES)];
+  lds_char* smem = (lds_char*)smem_raw;
+  typedef __attribute__((address_space(3))) float lds_f32;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int q = wave & 3, half = wave >> 2;
+  const int rbA = (wave / WN) * (TB / 2), rbB = (wave % WN) * 64;
+
+  // the tile: rows [m0, m_end) of group g, columns from n0 on
+  int tm, tn;
+  int64_t m0, m_end = p.M;
+  const char* B = p.B;
+  const float* sb = p.sb;
+  if (p.offsets) {
+    const int tiles = count_tiles<TB>(p.offsets, p.groups, p.M, lane);
+    if ((int64_t)blockIdx.x >= (int64_t)tiles * p.tiles_n) return;  // (the whole workgroup)
+    grouped_tile<4>(xcd_order(blockIdx.x, tiles * p.tiles_n), tiles, p.tiles_n, tm, tn);
+    const GroupTile w = find_tile<TB>(p.offsets, p.groups, p.M, tm, lane);
+    m0 = w.r0 + (int64_t)w.t * TB;
+    m_end = w.r1;
+    if (m0 >= m_end) return;
+    B += w.g * p.strideB;
+    sb += w.g * p.strideSB;
+  } else {
+    grouped_tile<4>(xcd_order(blockIdx.x, p.tiles_m * p.tiles_n), p.tiles_m, p.tiles_n, tm, tn);
+    m0 = (int64_t)tm * TB;
+  }
+  tn = __builtin_amdgcn_readfirstlane(tn);
+  const int64_t n0 = (int64_t)tn * TB;
+  const int nk = (int)((p.K + KT - 1) / KT);
+
+  DmaA da;
+  DmaB db;
+  da.init(p.A, p.lda, m_end, m0, p.K, q, lane);
+  db.init(B, p.ldb, p.N, n0, p.K, q, lane);
+  // Scales of a K tile: the first half of the wavefronts loads those of the rows, the second those
+  // of the columns, one for each lane.  (Past the end of either: zeros or another's, for outputs that
+  // are not stored.)
+  const bool of_rows = wave < NWAVES / 2;
+  const int sc = (wave % (NWAVES / 2)) * 64 + lane;  // row or column of the tile
+  __amdgpu_buffer_rsrc_t srs;
+  uint32_t soff, sstride;
+  {
+    const int64_t nb = (p.N + BLKB - 1) / BLKB, c0 = n0 / BLKB;
+    const int64_t cnt = of_rows ? min(m_end - m0, (int64_t)TB) : min(nb - c0, (int64_t)(TB / BLKB));
+    const int64_t ld = of_rows ? p.ldsa : p.ldsb, x0 = of_rows ? m0 : c0;
+    const float* base = of_rows ? p.sa : sb;
+    const int x = of_rows ? sc : sc / BLKB;
+    if ((of_rows ? LA : LB) == LAYOUT_K) {
+      srs = make_rsrc(base + x0 * ld, (uint32_t)(((cnt - 1) * ld + nk) * 4));
+      soff = (uint32_t)(x * ld * 4);
+      sstride = 4;
+    } else {
+      srs = make_rsrc(base + x0, (uint32_t)(((nk - 1) * ld + cnt) * 4));
+      soff = (uint32_t)(x * 4);
+      sstride = (uint32_t)(ld * 4);
+    }
+  }
+  auto stage = [&](int t) { return smem + (t & 1) * (2 * STAGE + SCALES); };
+  auto issue = [&](int t) {
+    lds_char* st = stage(t);
+    da.template issue<IA>(st, t, IA * half, q);
+    db.template issue<IA>(st + STAGE, t, IA * half, q);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(srs, (__attribute__((address_space(3))) void*)(st + 2 * STAGE + wave * 256), 4,
+                                             t < nk ? soff + (uint32_t)t * sstride : BUF_OOB, 0, 0, 0);
+  };
+
+  f32x4 acc[WTM][WTN];
+#pragma unroll
+  for (int i = 0; i < WTM; ++i)
+#pragma unroll
+    for (int j = 0; j < WTN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+  issue(0);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  barrier_lds();
+  issue(1);
+  typename Op::frag_t fb[WTN];
+  i32x8 rawa[1];
+  auto read_b = [&](int t) {
+    i32x8 r[WTN];
+    read_frags<LB, TB, WTN>(stage(t) + STAGE, rbB, lane, r);
+#pragma unroll
+    for (int j = 0; j < WTN; ++j) fb[j] = Op::b(r[j]);
+  };
+  read_b(0);
+  read_frags<LA, TB, 1>(stage(0), rbA, lane, rawa);
+  for (int t = 0; t < nk; ++t) {
+    const lds_char* st = stage(t);
+    const lds_f32* ssa = (const lds_f32*)(st + 2 * STAGE);
+    const lds_f32* ssb = ssa + TB;
+    float fs[WTM];
+    f32x4 cs[BLKB == 1 ? WTN : 1];
+    {
+      const float sbu = BLKB == 1 ? 1.0f : ssb[rbB];
+#pragma unroll
+      for (int i = 0; i < WTM; ++i) fs[i] = ssa[rbA + 16 * i + (lane & 15)] * sbu;
+      if constexpr (BLKB == 1) {
+        typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+#pragma unroll
+        for (int j = 0; j < WTN; ++j) cs[j] = *(const lds_f32x4*)(ssb + rbB + 16 * j + 4 * (lane >> 4));
+      }
+    }
+    f32x4 part[2][WTN];
+    auto add = [&](int i) {
+#pragma unroll
+      for (int j = 0; j < WTN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float s = BLKB == 1 ? fs[i] * cs[BLKB == 1 ? j : 0][e] : fs[i];
+          acc[i][j][e] = __builtin_fmaf(part[i & 1][j][e], s, acc[i][j][e]);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < WTM; ++i) {
+      const typename Op::frag_t fa = Op::a(rawa[0]);
+      if (i + 1 < WTM) read_frags<LA, TB, 1>(st, rbA + 16 * (i + 1), lane, rawa);
+      if (i == WTM - 2) {
+        // the last fragments are on their way: this stage is free once every wavefront is here,
+        // and K tile t + 1 (whose loads went out a K tile ago) has landed
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        barrier_lds();
+        issue(t + 2);
+      }
+#pragma unroll
+      for (int j = 0; j < WTN; ++j) part[i & 1][j] = Op::block(fb[j], fa);
+      if (i > 0) add(i - 1);
+    }
+    read_frags<LA, TB, 1>(stage(t + 1), rbA, lane, rawa);
+    read_b(t + 1);  // (past the end: zeros, not used)
+    add(WTM - 1);
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no LDS DMA outstanding at exit
+  barrier_lds();
+
+  // Epilogue: lane l of block (i, j) holds D[16 i + l % 16][16 j + 4 (l / 16) .. + 3].  32 rows of a
+  // wavefront at a time go through its 8 KiB of LDS, so that 16 lanes then store a row's 64 columns.
+  typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+  lds_char* wbuf = smem + wave * 8192;
+  const int rr = lane >> 4, cc = lane & 15;
+#pragma unroll
+  for (int i = 0; i < WTM; i += 2) {
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < WTN; ++j) {
+        const int r = 16 * h + cc, ch = 4 * j + rr;
+        *(lds_f32x4*)(wbuf + r * 256 + ((ch ^ (r & 15)) << 4)) = acc[i + h][j];
+      }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    f32x4 v[8];
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+      const int r = 4 * t + rr;
+      v[t] = *(const lds_f32x4*)(wbuf + r * 256 + ((cc ^ (r & 15)) << 4));
+    }
+    const int64_t m = m0 + rbA + 16 * i + rr, n = n0 + rbB + 4 * cc;
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+      if (m + 4 * t < m_end && n < p.N) group_store4(p, 0, m + 4 * t, n, v[t]);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
+}
+
+template <class Op, int LA, int LB, int BLKB, int TB>
+hipError_t launch_one(const GroupArgs& a0, hipStream_t s) {
+  GroupArgs a = a0;
+  a.tiles_m = (int)most_tiles(a.M, a.groups, TB, a.offsets != nullptr);
+  a.tiles_n = (int)((a.N + TB - 1) / TB);
+  const int64_t blocks = (int64_t)a.tiles_m * a.tiles_n;
+  if (blocks >= MANY_TILES) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((f8_blocks_kernel<Op, LA, LB, BLKB, TB>), dim3((unsigned)blocks), dim3(2 * TB), 0, s, a);
+  return hipGetLastError();
+}
+
+// A layer's output, its input gradient and its weight gradient.
+template <template <int> class Op, int FA, int TB>
+hipError_t launch_kinds(int la, int lb, int blockB, const GroupArgs& a, hipStream_t s) {
+  if (la == LAYOUT_MN) return launch_one<Op<FA>, LAYOUT_MN, LAYOUT_MN, 1, TB>(a, s);
+  return lb == LAYOUT_K ? launch_one<Op<FA>, LAYOUT_K, LAYOUT_K, 128, TB>(a, s)
+                        : launch_one<Op<FA>, LAYOUT_K, LAYOUT_MN, 128, TB>(a, s);
+}
+
+}  // namespace f8b
+}  // namespace mcg
