@@ -43,18 +43,27 @@ GroupPlan plan_grouped(int dt, int la, int lb, const GroupArgs& a, int num_cu) {
     if (a.out == OUT_BF16 && cdiv(a.M, 256) * cdiv(a.N, 256) >= num_cu / 2) return {KERNEL_FAST, 256};
     return {KERNEL_MID, 128};
   }
+  if (eb == 2 && chunks_ok(2, a, la, lb, 2) && a.M / a.groups > 32) {
+    const int tile = cdiv(a.M, 256) * cdiv(a.N, 256) >= num_cu / 2 ? 256 : 128;
+    return {tile == 256 ? KERNEL_FAST : KERNEL_MID, tile};
+  }
   return {KERNEL_GENERAL, general_tile_rows(a.M / a.groups)};
 }
 
 GroupPlan plan_grouped_grad(int dt, const GroupArgs& a, int num_cu) {
   const int64_t eb = elem_bytes(dt);
   if (a.K == 0 || a.M * eb < 16 || a.N * eb < 16) return {KERNEL_TINY, 1};
+  if (chunks_ok(2, a, MCG_MN_CONTIG, MCG_MN_CONTIG, 2) && a.M >= 64 && a.N >= 64) {
+    const int tile = a.groups * cdiv(a.M, 256) * cdiv(a.N, 256) >= num_cu / 2 ? 256 : 128;
+    return {tile == 256 ? KERNEL_FAST : KERNEL_MID, tile};
+  }
   return {KERNEL_GENERAL, general_tile_rows(a.M)};
 }
 
 hipError_t launch_grouped(int dt, int la, int lb, const GroupArgs& a, int num_cu, hipStream_t s) {
   const GroupPlan p = plan_grouped(dt, la, lb, a, num_cu);
   if (p.kernel == KERNEL_TINY) return launch_group_tiny(dt, la, lb, false, a, s);
+  if (elem_bytes(dt) == 2 && p.kernel != KERNEL_GENERAL) return launch_group_pipe(dt, lb, false, p.tile, a, s);
   if (p.kernel == KERNEL_FAST) return launch_f8_blocks_256(dt, la, lb, a.blockB, a, s);
   if (p.kernel == KERNEL_MID) return launch_f8_blocks_128(dt, la, lb, a.blockB, a.out != OUT_BF16, a, s);
   return launch_group_general(dt, la, lb, false, a, p.tile, s);
@@ -63,6 +72,7 @@ hipError_t launch_grouped(int dt, int la, int lb, const GroupArgs& a, int num_cu
 hipError_t launch_grouped_grad(int dt, const GroupArgs& a, int num_cu, hipStream_t s) {
   const GroupPlan p = plan_grouped_grad(dt, a, num_cu);
   if (p.kernel == KERNEL_TINY) return launch_group_tiny(dt, MCG_MN_CONTIG, MCG_MN_CONTIG, true, a, s);
+  if (p.kernel != KERNEL_GENERAL) return launch_group_pipe(dt, MCG_MN_CONTIG, true, p.tile, a, s);
   return launch_group_general(dt, MCG_MN_CONTIG, MCG_MN_CONTIG, true, a, p.tile, s);
 }
 

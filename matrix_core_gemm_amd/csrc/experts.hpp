@@ -61,6 +61,9 @@ hipError_t launch_blocks_dequant(int dtQ, int dt, int bm, int bn, const BlocksAr
 hipError_t launch_f8_blocks_256(int dtA, int la, int lb, int blockB, const GroupArgs& a, hipStream_t s);
 hipError_t launch_f8_blocks_128(int dtA, int la, int lb, int blockB, bool wide, const GroupArgs& a, hipStream_t s);
 
+// The pipelined 16-bit products by group (group_pipe_kernel.hpp), 256 x 256 or 128 x 128 tiles.
+hipError_t launch_group_pipe(int dt, int lb, bool grad, int tile, const GroupArgs& a, hipStream_t s);
+
 // The choice of a kernel, and its launch (expert_plan.cpp).
 GroupPlan plan_grouped(int dt, int la, int lb, const GroupArgs& a, int num_cu);
 GroupPlan plan_grouped_grad(int dt, const GroupArgs& a, int num_cu);
