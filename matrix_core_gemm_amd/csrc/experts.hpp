@@ -55,13 +55,15 @@ struct BlocksArgs {
 hipError_t launch_blocks_quant(int dt, int dtQ, int bm, int bn, const BlocksArgs& a, hipStream_t s);
 hipError_t launch_blocks_dequant(int dtQ, int dt, int bm, int bn, const BlocksArgs& a, hipStream_t s);
 
-// The pipelined product of block-scaled 8-bit floats (f8_blocks_kernel.hpp), 256 x 256 and 128 x 128
-// tiles: A and B K-contiguous or B MN-contiguous with blockB 128, or both MN-contiguous with blockB 1.
-// wide: exact products (f16 and binary32 D).
-hipError_t launch_f8_blocks_256(int dtA, int la, int lb, int blockB, const GroupArgs& a, hipStream_t s);
-hipError_t launch_f8_blocks_128(int dtA, int la, int lb, int blockB, bool wide, const GroupArgs& a, hipStream_t s);
+// The pipelined product of block-scaled 8-bit floats (f8_blocks_kernel.hpp), 256 x 256, 128 x 128 and
+// 64 x 128 tiles: A and B K-contiguous or B MN-contiguous with blockB 128, or both MN-contiguous with
+// blockB 1.  wide: exact products (f16 and binary32 D).
+hipError_t launch_f8_blocks_256(int dtA, int la, int lb, const GroupArgs& a, hipStream_t s);
+hipError_t launch_f8_blocks_128(int dtA, int la, int lb, bool wide, const GroupArgs& a, hipStream_t s);
+hipError_t launch_f8_blocks_64(int dtA, int la, int lb, bool wide, const GroupArgs& a, hipStream_t s);
 
-// The pipelined 16-bit products by group (group_pipe_kernel.hpp), 256 x 256 or 128 x 128 tiles.
+// The pipelined 16-bit products by group (group_pipe_kernel.hpp), 256 x 256, 128 x 128 or (rows) 64 x 128
+// tiles.
 hipError_t launch_group_pipe(int dt, int lb, bool grad, int tile, const GroupArgs& a, hipStream_t s);
 
 // The choice of a kernel, and its launch (expert_plan.cpp).

@@ -3,9 +3,9 @@
 
 namespace mcg {
 
-hipError_t launch_f8_blocks_256(int dtA, int la, int lb, int blockB, const GroupArgs& a, hipStream_t s) {
-  return dtA == DT_E4M3 ? f8b::launch_kinds<f8b::Native, 0, 256>(la, lb, blockB, a, s)
-                        : f8b::launch_kinds<f8b::Native, 1, 256>(la, lb, blockB, a, s);
+hipError_t launch_f8_blocks_256(int dtA, int la, int lb, const GroupArgs& a, hipStream_t s) {
+  return dtA == DT_E4M3 ? f8b::launch_kinds<f8b::Native<0>, 256, 256>(la, lb, a, s)
+                        : f8b::launch_kinds<f8b::Native<1>, 256, 256>(la, lb, a, s);
 }
 
 }  // namespace mcg

@@ -41,8 +41,10 @@ constexpr int KT = SCALE_BLOCK;  // k (and bytes) of a K tile
 // in distinct banks.  The pattern repeats every 32 rows.
 template <int TB>
 __device__ __forceinline__ int mn_swz(int row) {
+  static_assert(TB == 256 || TB == 128 || TB == 64, "tile");
   if constexpr (TB == 256) return (row & 7) | (8 * ((row >> 4) & 1));
-  else return ((row >> 1) & 3) | (4 * ((row >> 4) & 1));
+  else if constexpr (TB == 128) return ((row >> 1) & 3) | (4 * ((row >> 4) & 1));
+  else return ((row >> 2) & 1) | (2 * ((row >> 4) & 1));
 }
 
 // HBM -> LDS loader of one operand's K tiles: wavefront q of 4 writes LDS bytes
@@ -160,61 +162,47 @@ struct Wide {
   }
 };
 
-// BLKB: columns of B under one scale (128 or 1).
-template <class Op, int LA, int LB, int BLKB, int TB>
-__global__ __launch_bounds__(2 * TB) __attribute__((amdgpu_waves_per_eu(2, 2))) void f8_blocks_kernel(GroupArgs p) {
+// LDS stages of K tiles, codes and scales: a tile of half as many rows as columns has room for a third,
+// which a group's short last tile needs, since its instructions do not cover a load's way.
+template <int TBM, int TB>
+struct Ring {
+  static constexpr int STAGE_A = TBM * KT, CODES = STAGE_A + TB * KT, STAGE = CODES + (TBM + TB) * 4;
+  static constexpr int NS = TBM < TB ? 3 : 2, BYTES = NS * STAGE;
+};
+
+// The tile TBM x TB of D from row m0 (those below m_end) and column n0 on: TB / 32 wavefronts, two
+// down the rows.  BLKB: columns of B under one scale (128 or 1).
+template <class Op, int LA, int LB, int BLKB, int TBM, int TB>
+__device__ __forceinline__ void f8_tile_work(const GroupArgs& p, lds_char* smem, const char* B, const float* sb, int64_t m0,
+                                             int64_t m_end, int64_t n0, int wave, int lane) {
   constexpr int NWAVES = TB / 32, WN = TB / 64;  // wavefronts, 2 x WN of them
-  constexpr int WTM = TB / 32, WTN = 4;          // 16 x 16 blocks of a wavefront
-  constexpr int STAGE = TB * KT, SCALES = 2 * TB * 4;
-  using DmaA = TileDma<LA, TB>;
+  constexpr int WTM = TBM / 32, WTN = 4;         // 16 x 16 blocks of a wavefront
+  using RG = Ring<TBM, TB>;
+  constexpr int NS = RG::NS;
+  using DmaA = TileDma<LA, TBM>;
   using DmaB = TileDma<LB, TB>;
-  constexpr int HALVES = NWAVES / 4, IA = DmaA::INSTR / HALVES;  // instructions per wavefront, operand and K tile
-  __shared__ __attribute__((aligned(1024))) char smem_raw[2 * (2 * STAGE + SCALES)];
-  lds_char* smem = (lds_char*)smem_raw;
+  constexpr int HALVES = NWAVES / 4, IA = DmaA::INSTR / HALVES, IB = DmaB::INSTR / HALVES;
+  constexpr int NL = IA + IB + 1;  // load instructions per wavefront and K tile
   typedef __attribute__((address_space(3))) float lds_f32;
-
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = wave & 3, half = wave >> 2;
-  const int rbA = (wave / WN) * (TB / 2), rbB = (wave % WN) * 64;
-
-  // the tile: rows [m0, m_end) of group g, columns from n0 on
-  int tm, tn;
-  int64_t m0, m_end = p.M;
-  const char* B = p.B;
-  const float* sb = p.sb;
-  if (p.offsets) {
-    const int tiles = count_tiles<TB>(p.offsets, p.groups, p.M, lane);
-    if ((int64_t)blockIdx.x >= (int64_t)tiles * p.tiles_n) return;  // (the whole workgroup)
-    grouped_tile<4>(xcd_order(blockIdx.x, tiles * p.tiles_n), tiles, p.tiles_n, tm, tn);
-    const GroupTile w = find_tile<TB>(p.offsets, p.groups, p.M, tm, lane);
-    m0 = w.r0 + (int64_t)w.t * TB;
-    m_end = w.r1;
-    if (m0 >= m_end) return;
-    B += w.g * p.strideB;
-    sb += w.g * p.strideSB;
-  } else {
-    grouped_tile<4>(xcd_order(blockIdx.x, p.tiles_m * p.tiles_n), p.tiles_m, p.tiles_n, tm, tn);
-    m0 = (int64_t)tm * TB;
-  }
-  tn = __builtin_amdgcn_readfirstlane(tn);
-  const int64_t n0 = (int64_t)tn * TB;
+  const int rbA = (wave / WN) * (TBM / 2), rbB = (wave % WN) * 64;
   const int nk = (int)((p.K + KT - 1) / KT);
 
   DmaA da;
   DmaB db;
   da.init(p.A, p.lda, m_end, m0, p.K, q, lane);
   db.init(B, p.ldb, p.N, n0, p.K, q, lane);
-  // Scales of a K tile: the first half of the wavefronts loads those of the rows, the second those
-  // of the columns, one for each lane.  (Past the end of either: zeros or another's, for outputs that
-  // are not stored.)
-  const bool of_rows = wave < NWAVES / 2;
-  const int sc = (wave % (NWAVES / 2)) * 64 + lane;  // row or column of the tile
+  // Scales of a K tile: the first wavefronts load those of the rows, the next those of the
+  // columns, one for each lane, the others (of a tile of few rows) the same as the last of these.
+  // (Past the end of either: zeros or another's, for outputs that are not stored.)
+  const int ws = min(wave, (TBM + TB) / 64 - 1);
+  const bool of_rows = ws < TBM / 64;
+  const int sc = (of_rows ? ws : ws - TBM / 64) * 64 + lane;  // row or column of the tile
   __amdgpu_buffer_rsrc_t srs;
   uint32_t soff, sstride;
   {
     const int64_t nb = (p.N + BLKB - 1) / BLKB, c0 = n0 / BLKB;
-    const int64_t cnt = of_rows ? min(m_end - m0, (int64_t)TB) : min(nb - c0, (int64_t)(TB / BLKB));
+    const int64_t cnt = of_rows ? min(m_end - m0, (int64_t)TBM) : min(nb - c0, (int64_t)(TB / BLKB));
     const int64_t ld = of_rows ? p.ldsa : p.ldsb, x0 = of_rows ? m0 : c0;
     const float* base = of_rows ? p.sa : sb;
     const int x = of_rows ? sc : sc / BLKB;
@@ -228,12 +216,12 @@ __global__ __launch_bounds__(2 * TB) __attribute__((amdgpu_waves_per_eu(2, 2))) 
       sstride = (uint32_t)(ld * 4);
     }
   }
-  auto stage = [&](int t) { return smem + (t & 1) * (2 * STAGE + SCALES); };
-  auto issue = [&](int t) {
+  auto stage = [&](int t) { return smem + (t % NS) * RG::STAGE; };
+  auto issue = [&](int t) {  // (K tiles past the end: zeros)
     lds_char* st = stage(t);
     da.template issue<IA>(st, t, IA * half, q);
-    db.template issue<IA>(st + STAGE, t, IA * half, q);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(srs, (__attribute__((address_space(3))) void*)(st + 2 * STAGE + wave * 256), 4,
+    db.template issue<IB>(st + RG::STAGE_A, t, IB * half, q);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(srs, (__attribute__((address_space(3))) void*)(st + RG::CODES + ws * 256), 4,
                                              t < nk ? soff + (uint32_t)t * sstride : BUF_OOB, 0, 0, 0);
   };
 
@@ -243,65 +231,79 @@ __global__ __launch_bounds__(2 * TB) __attribute__((amdgpu_waves_per_eu(2, 2))) 
 #pragma unroll
     for (int j = 0; j < WTN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-  issue(0);
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+  for (int t = 0; t < NS; ++t) issue(t);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 1) * NL) : "memory");  // own loads of K tile 0
   barrier_lds();
-  issue(1);
   typename Op::frag_t fb[WTN];
   i32x8 rawa[1];
   auto read_b = [&](int t) {
     i32x8 r[WTN];
-    read_frags<LB, TB, WTN>(stage(t) + STAGE, rbB, lane, r);
+    read_frags<LB, TB, WTN>(stage(t) + RG::STAGE_A, rbB, lane, r);
 #pragma unroll
     for (int j = 0; j < WTN; ++j) fb[j] = Op::b(r[j]);
   };
   read_b(0);
-  read_frags<LA, TB, 1>(stage(0), rbA, lane, rawa);
-  for (int t = 0; t < nk; ++t) {
-    const lds_char* st = stage(t);
-    const lds_f32* ssa = (const lds_f32*)(st + 2 * STAGE);
-    const lds_f32* ssb = ssa + TB;
-    float fs[WTM];
-    f32x4 cs[BLKB == 1 ? WTN : 1];
-    {
-      const float sbu = BLKB == 1 ? 1.0f : ssb[rbB];
+  read_frags<LA, TBM, 1>(stage(0), rbA, lane, rawa);
+  // The K tiles, with LIVE of the wavefront's WTM blocks of rows inside the tile (in pairs): a
+  // group's last tile costs the instructions of its own rows only.  All wavefronts take the same
+  // barriers.
+  auto k_loop = [&](auto pairs) {
+    constexpr int LIVE = 2 * decltype(pairs)::value, LAST = LIVE > 2 ? LIVE - 2 : 0;
+    for (int t = 0; t < nk; ++t) {
+      const lds_char* st = stage(t);
+      const lds_f32* ssa = (const lds_f32*)(st + RG::CODES);
+      const lds_f32* ssb = ssa + TBM;
+      float fs[LIVE > 0 ? LIVE : 1];
+      f32x4 cs[BLKB == 1 ? WTN : 1];
+      if (LIVE > 0) {
+        const float sbu = BLKB == 1 ? 1.0f : ssb[rbB];
 #pragma unroll
-      for (int i = 0; i < WTM; ++i) fs[i] = ssa[rbA + 16 * i + (lane & 15)] * sbu;
-      if constexpr (BLKB == 1) {
-        typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+        for (int i = 0; i < LIVE; ++i) fs[i] = ssa[rbA + 16 * i + (lane & 15)] * sbu;
+        if constexpr (BLKB == 1) {
+          typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
 #pragma unroll
-        for (int j = 0; j < WTN; ++j) cs[j] = *(const lds_f32x4*)(ssb + rbB + 16 * j + 4 * (lane >> 4));
-      }
-    }
-    f32x4 part[2][WTN];
-    auto add = [&](int i) {
-#pragma unroll
-      for (int j = 0; j < WTN; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float s = BLKB == 1 ? fs[i] * cs[BLKB == 1 ? j : 0][e] : fs[i];
-          acc[i][j][e] = __builtin_fmaf(part[i & 1][j][e], s, acc[i][j][e]);
+          for (int j = 0; j < WTN; ++j) cs[j] = *(const lds_f32x4*)(ssb + rbB + 16 * j + 4 * (lane >> 4));
         }
-    };
-#pragma unroll
-    for (int i = 0; i < WTM; ++i) {
-      const typename Op::frag_t fa = Op::a(rawa[0]);
-      if (i + 1 < WTM) read_frags<LA, TB, 1>(st, rbA + 16 * (i + 1), lane, rawa);
-      if (i == WTM - 2) {
-        // the last fragments are on their way: this stage is free once every wavefront is here,
-        // and K tile t + 1 (whose loads went out a K tile ago) has landed
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        barrier_lds();
-        issue(t + 2);
       }
+      f32x4 part[2][WTN];
+      auto add = [&](int i) {
 #pragma unroll
-      for (int j = 0; j < WTN; ++j) part[i & 1][j] = Op::block(fb[j], fa);
-      if (i > 0) add(i - 1);
+        for (int j = 0; j < WTN; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float s = BLKB == 1 ? fs[i] * cs[BLKB == 1 ? j : 0][e] : fs[i];
+            acc[i][j][e] = __builtin_fmaf(part[i & 1][j][e], s, acc[i][j][e]);
+          }
+      };
+#pragma unroll
+      for (int i = 0; i < (LIVE > 0 ? LIVE : 1); ++i) {
+        typename Op::frag_t fa;
+        if (i < LIVE) fa = Op::a(rawa[0]);
+        if (i + 1 < LIVE) read_frags<LA, TBM, 1>(st, rbA + 16 * (i + 1), lane, rawa);
+        if (i == LAST) {
+          // the last fragments are on their way: this stage is free once every wavefront is here,
+          // and K tile t + 1 has landed once all but the NS - 2 newest K tiles' loads have
+          asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 2) * NL) : "memory");
+          barrier_lds();
+          issue(t + NS);
+        }
+        if (i < LIVE) {
+#pragma unroll
+          for (int j = 0; j < WTN; ++j) part[i & 1][j] = Op::block(fb[j], fa);
+          if (i > 0) add(i - 1);
+        }
+      }
+      if (LIVE > 0) {
+        read_frags<LA, TBM, 1>(stage(t + 1), rbA, lane, rawa);
+        read_b(t + 1);  // (past the end: zeros, not used)
+        add(LIVE - 1);
+      }
     }
-    read_frags<LA, TB, 1>(stage(t + 1), rbA, lane, rawa);
-    read_b(t + 1);  // (past the end: zeros, not used)
-    add(WTM - 1);
-  }
+  };
+  const int64_t left = (m_end - m0 - rbA + 31) / 32;
+  if constexpr (LA == LAYOUT_MN) k_loop(std::integral_constant<int, WTM / 2>{});  // (no groups)
+  else with_live<WTM / 2>(left < WTM / 2 ? (int)left : WTM / 2, k_loop);
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no LDS DMA outstanding at exit
   barrier_lds();
 
@@ -328,30 +330,53 @@ __global__ __launch_bounds__(2 * TB) __attribute__((amdgpu_waves_per_eu(2, 2))) 
       v[t] = *(const lds_f32x4*)(wbuf + r * 256 + ((cc ^ (r & 15)) << 4));
     }
     const int64_t m = m0 + rbA + 16 * i + rr, n = n0 + rbB + 4 * cc;
-#pragma unroll
-    for (int t = 0; t < 8; ++t)
-      if (m + 4 * t < m_end && n < p.N) group_store4(p, 0, m + 4 * t, n, v[t]);
+    group_store_rows(p, 0, m, m_end, n, v);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 }
 
-template <class Op, int LA, int LB, int BLKB, int TB>
+// TBM x TB tiles (256 x 256, 128 x 128, 64 x 128); with TBM = TB a group's last one of up to TB / 2 rows is
+// TB / 2 x TB.
+template <class Op, int LA, int LB, int BLKB, int TBM, int TB>
+__global__ __launch_bounds__(2 * TB) __attribute__((amdgpu_waves_per_eu(2, 2))) void f8_blocks_kernel(GroupArgs p) {
+  constexpr bool GROUPS = LA == LAYOUT_K;  // (the weight gradient has none)
+  constexpr int LDS = !GROUPS || Ring<TBM, TB>::BYTES > Ring<TB / 2, TB>::BYTES ? Ring<TBM, TB>::BYTES : Ring<TB / 2, TB>::BYTES;
+  __shared__ __attribute__((aligned(1024))) char smem_raw[LDS];
+  lds_char* smem = (lds_char*)smem_raw;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  if (GROUPS && p.offsets) {
+    const PipeTile w = pipe_tile<TBM>(p.offsets, p.groups, p.M, p.tiles_n, blockIdx.x, lane);
+    if (w.m0 >= w.r1) return;  // (the whole workgroup)
+    const char* B = p.B + w.g * p.strideB;
+    const float* sb = p.sb + w.g * p.strideSB;
+    if (TBM == TB && w.r1 - w.m0 > TB / 2)
+      f8_tile_work<Op, LA, LB, BLKB, TB, TB>(p, smem, B, sb, w.m0, w.r1, (int64_t)w.tn * TB, wave, lane);
+    else
+      f8_tile_work<Op, LA, LB, BLKB, TB / 2, TB>(p, smem, B, sb, w.m0, w.r1, (int64_t)w.tn * TB, wave, lane);
+  } else {
+    int tm, tn;
+    grouped_tile<4>(xcd_order(blockIdx.x, p.tiles_m * p.tiles_n), p.tiles_m, p.tiles_n, tm, tn);
+    f8_tile_work<Op, LA, LB, BLKB, TBM, TB>(p, smem, p.B, p.sb, (int64_t)tm * TBM, p.M, (int64_t)tn * TB, wave, lane);
+  }
+}
+
+template <class Op, int LA, int LB, int BLKB, int TBM, int TB>
 hipError_t launch_one(const GroupArgs& a0, hipStream_t s) {
   GroupArgs a = a0;
-  a.tiles_m = (int)most_tiles(a.M, a.groups, TB, a.offsets != nullptr);
+  a.tiles_m = (int)most_tiles(a.M, a.groups, TBM, a.offsets != nullptr);
   a.tiles_n = (int)((a.N + TB - 1) / TB);
-  const int64_t blocks = (int64_t)a.tiles_m * a.tiles_n;
+  const int64_t blocks = a.offsets ? slice_blocks(a.tiles_m, a.tiles_n) : (int64_t)a.tiles_m * a.tiles_n;
   if (blocks >= MANY_TILES) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((f8_blocks_kernel<Op, LA, LB, BLKB, TB>), dim3((unsigned)blocks), dim3(2 * TB), 0, s, a);
+  hipLaunchKernelGGL((f8_blocks_kernel<Op, LA, LB, BLKB, TBM, TB>), dim3((unsigned)blocks), dim3(2 * TB), 0, s, a);
   return hipGetLastError();
 }
 
 // A layer's output, its input gradient and its weight gradient.
-template <template <int> class Op, int FA, int TB>
-hipError_t launch_kinds(int la, int lb, int blockB, const GroupArgs& a, hipStream_t s) {
-  if (la == LAYOUT_MN) return launch_one<Op<FA>, LAYOUT_MN, LAYOUT_MN, 1, TB>(a, s);
-  return lb == LAYOUT_K ? launch_one<Op<FA>, LAYOUT_K, LAYOUT_K, 128, TB>(a, s)
-                        : launch_one<Op<FA>, LAYOUT_K, LAYOUT_MN, 128, TB>(a, s);
+template <class Op, int TBM, int TB>
+hipError_t launch_kinds(int la, int lb, const GroupArgs& a, hipStream_t s) {
+  if (la == LAYOUT_MN) return launch_one<Op, LAYOUT_MN, LAYOUT_MN, 1, TBM, TB>(a, s);
+  return lb == LAYOUT_K ? launch_one<Op, LAYOUT_K, LAYOUT_K, 128, TBM, TB>(a, s)
+                        : launch_one<Op, LAYOUT_K, LAYOUT_MN, 128, TBM, TB>(a, s);
 }
 
 }  // namespace f8b

@@ -3,12 +3,12 @@
 
 namespace mcg {
 
-hipError_t launch_f8_blocks_128(int dtA, int la, int lb, int blockB, bool wide, const GroupArgs& a, hipStream_t s) {
+hipError_t launch_f8_blocks_128(int dtA, int la, int lb, bool wide, const GroupArgs& a, hipStream_t s) {
   if (wide)
-    return dtA == DT_E4M3 ? f8b::launch_kinds<f8b::Wide, 0, 128>(la, lb, blockB, a, s)
-                          : f8b::launch_kinds<f8b::Wide, 1, 128>(la, lb, blockB, a, s);
-  return dtA == DT_E4M3 ? f8b::launch_kinds<f8b::Native, 0, 128>(la, lb, blockB, a, s)
-                        : f8b::launch_kinds<f8b::Native, 1, 128>(la, lb, blockB, a, s);
+    return dtA == DT_E4M3 ? f8b::launch_kinds<f8b::Wide<0>, 128, 128>(la, lb, a, s)
+                          : f8b::launch_kinds<f8b::Wide<1>, 128, 128>(la, lb, a, s);
+  return dtA == DT_E4M3 ? f8b::launch_kinds<f8b::Native<0>, 128, 128>(la, lb, a, s)
+                        : f8b::launch_kinds<f8b::Native<1>, 128, 128>(la, lb, a, s);
 }
 
 }  // namespace mcg

@@ -52,49 +52,28 @@ __device__ __forceinline__ void read_frags(const lds_char* tile, int rb, int lan
   }
 }
 
-template <class Op, int LA, int LB, int TB, bool GRAD>
-__global__ __launch_bounds__(2 * TB) __attribute__((amdgpu_waves_per_eu(2, 2))) void group_pipe_kernel(GroupArgs p) {
+// LDS stages of K tiles: a tile of half as many rows as columns has room for a third, which a group's
+// short last tile needs, since its instructions do not cover a load's way.
+template <int TBM, int TB>
+struct Ring {
+  static constexpr int STAGE_A = TBM * KTB, STAGE_B = TB * KTB;
+  static constexpr int NA = TBM < TB ? 3 : 2, NB = 3, BYTES = NA * STAGE_A + NB * STAGE_B;
+};
+
+// The tile TBM x TB of D from row m0 (those below m_end) and column n0 on: TB / 32 wavefronts, two
+// down the rows.  A: its first row of m0 = 0 (K-contiguous) or of k = 0.
+template <class Op, int LA, int LB, int TBM, int TB, bool GRAD>
+__device__ __forceinline__ void pipe_tile_work(const GroupArgs& p, lds_char* smem, const char* A, const char* B, int64_t K,
+                                               int64_t m0, int64_t m_end, int64_t n0, int64_t dbase, int wave, int lane) {
   constexpr int NWAVES = TB / 32, WN = TB / 64;  // wavefronts, 2 x WN of them
-  constexpr int WTM = TB / 64, WTN = 2;          // 32 x 32 blocks of a wavefront
-  constexpr int STAGE = TB * KTB;
-  using DmaA = LineLoader<2, LA, TB, KTB>;
+  constexpr int WTM = TBM / 64, WTN = 2;         // 32 x 32 blocks of a wavefront
+  using RG = Ring<TBM, TB>;
+  constexpr int NA = RG::NA, NB = RG::NB;
+  using DmaA = LineLoader<2, LA, TBM, KTB>;
   using DmaB = LineLoader<2, LB, TB, KTB>;
-  constexpr int HALVES = NWAVES / 4, IA = DmaA::INSTR / HALVES;  // instructions per wavefront, operand and K tile
-  static_assert(DmaA::INSTR == DmaB::INSTR, "square tiles");
-  __shared__ __attribute__((aligned(1024))) char smem_raw[4 * STAGE];
-  lds_char* smem = (lds_char*)smem_raw;
-
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  constexpr int HALVES = NWAVES / 4, IA = DmaA::INSTR / HALVES, IB = DmaB::INSTR / HALVES;  // instructions per wavefront and K tile
   const int q = wave & 3, half = wave >> 2;
-  const int rbA = (wave / WN) * (TB / 2), rbB = (wave % WN) * 64;
-
-  // the tile: rows [m0, m_end) and columns from n0 on, over K values of k
-  int tm, tn;
-  int64_t m0, m_end = p.M, K = p.K, dbase = 0;
-  const char *A = p.A, *B = p.B;
-  if constexpr (GRAD) {
-    const int tiles = p.tiles_m * p.tiles_n, pid = xcd_order(blockIdx.x, tiles * p.groups);
-    const int g = __builtin_amdgcn_readfirstlane(pid / tiles);
-    grouped_tile<4>(pid - g * tiles, p.tiles_m, p.tiles_n, tm, tn);
-    const GroupRows r = group_rows(p.offsets, g, p.K);
-    m0 = (int64_t)tm * TB;
-    K = r.r1 - r.r0;
-    A += r.r0 * p.lda * 2;
-    B += r.r0 * p.ldb * 2;
-    dbase = g * p.strideD;
-  } else {
-    const int tiles = count_tiles<TB>(p.offsets, p.groups, p.M, lane);
-    if ((int64_t)blockIdx.x >= (int64_t)tiles * p.tiles_n) return;  // (the whole workgroup)
-    grouped_tile<4>(xcd_order(blockIdx.x, tiles * p.tiles_n), tiles, p.tiles_n, tm, tn);
-    const GroupTile w = find_tile<TB>(p.offsets, p.groups, p.M, tm, lane);
-    m0 = w.r0 + (int64_t)w.t * TB;
-    m_end = w.r1;
-    if (m0 >= m_end) return;
-    B += w.g * p.strideB * 2;
-  }
-  tn = __builtin_amdgcn_readfirstlane(tn);
-  const int64_t n0 = (int64_t)tn * TB;
+  const int rbA = (wave / WN) * (TBM / 2), rbB = (wave % WN) * 64;
   const int nk = (int)((K + KE - 1) / KE);
 
   f32x16 acc[WTM][WTN];
@@ -107,46 +86,69 @@ __global__ __launch_bounds__(2 * TB) __attribute__((amdgpu_waves_per_eu(2, 2))) 
     DmaA da;
     DmaB db;
     if constexpr (LA == LAYOUT_K)
-      da.init(A + m0 * p.lda * 2, (uint32_t)(min(m_end - m0, (int64_t)TB) * p.lda * 2), p.lda, K, q, lane);
+      da.init(A + m0 * p.lda * 2, (uint32_t)(min(m_end - m0, (int64_t)TBM) * p.lda * 2), p.lda, K, q, lane);
     else
       da.init(A + m0 * 2, mn_window(K, p.lda, m_end, m0, 2), p.lda, K, q, lane);
     if constexpr (LB == LAYOUT_K)
       db.init(B + n0 * p.ldb * 2, (uint32_t)(min(p.N - n0, (int64_t)TB) * p.ldb * 2), p.ldb, K, q, lane);
     else
       db.init(B + n0 * 2, mn_window(K, p.ldb, p.N, n0, 2), p.ldb, K, q, lane);
-    auto stage = [&](int t) { return smem + (t & 1) * (2 * STAGE); };
-    auto issue = [&](int t) {  // (K tiles past the end: zeros)
-      da.issue(stage(t), t, IA * half, IA, q);
-      db.issue(stage(t) + STAGE, t, IA * half, IA, q);
-    };
-    issue(0);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    barrier_lds();
-    issue(1);
-    i32x4 fb[WTN][4], fa[1][4], next[1][4];
-    read_frags<LB, TB, WTN>(stage(0) + STAGE, rbB, lane, fb);
-    read_frags<LA, TB, 1>(stage(0), rbA, lane, next);
-    for (int t = 0; t < nk; ++t) {
+    auto stage_a = [&](int t) { return smem + (t % NA) * RG::STAGE_A; };
+    auto stage_b = [&](int t) { return smem + NA * RG::STAGE_A + (t % NB) * RG::STAGE_B; };
+    // (K tiles past the end: zeros)
+    auto issue_a = [&](int t) { da.issue(stage_a(t), t, IA * half, IA, q); };
+    auto issue_b = [&](int t) { db.issue(stage_b(t), t, IB * half, IB, q); };
+    // loads of a wavefront that are younger than those of K tile t + 1 once K tiles t + NA - 1 of A and
+    // t + NB - 1 of B are on their way (A before B of the same step)
+    constexpr int NEWER = (NA - 2) * IA + (NB - 2) * IB;
 #pragma unroll
-      for (int i = 0; i < WTM; ++i) {
+    for (int t = 0; t < NB - NA; ++t) issue_b(t);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) fa[0][s] = next[0][s];
-        if (i + 1 < WTM) read_frags<LA, TB, 1>(stage(t), rbA + 32 * (i + 1), lane, next);
-        if (i == WTM - 2) {
-          // the last fragments are on their way: this stage is free once every wavefront is here,
-          // and K tile t + 1 (whose loads went out a K tile ago) has landed
-          asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-          barrier_lds();
-          issue(t + 2);
-        }
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-          for (int j = 0; j < WTN; ++j) Op::mma(acc[i][j], fb[j][s], fa[0][s]);
-      }
-      read_frags<LA, TB, 1>(stage(t + 1), rbA, lane, next);
-      read_frags<LB, TB, WTN>(stage(t + 1) + STAGE, rbB, lane, fb);  // (past the end: zeros, not used)
+    for (int t = 0; t < NA; ++t) {
+      issue_a(t);
+      issue_b(t + NB - NA);
     }
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NA - 1) * (IA + IB) + (NB > NA ? IB : 0)) : "memory");  // own loads of K tile 0
+    barrier_lds();
+    i32x4 fb[WTN][4], fa[1][4], next[1][4];
+    read_frags<LB, TB, WTN>(stage_b(0), rbB, lane, fb);
+    read_frags<LA, TBM, 1>(stage_a(0), rbA, lane, next);
+    // The K tiles, with LIVE of the wavefront's WTM blocks of rows inside the tile: a group's last
+    // tile costs the instructions of its own rows only.  All wavefronts take the same barriers.
+    auto k_loop = [&](auto live) {
+      constexpr int LIVE = decltype(live)::value, LAST = LIVE > 2 ? LIVE - 2 : 0;
+      for (int t = 0; t < nk; ++t) {
+#pragma unroll
+        for (int i = 0; i < (LIVE > 0 ? LIVE : 1); ++i) {
+          if (i < LIVE) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) fa[0][s] = next[0][s];
+          }
+          if (i + 1 < LIVE) read_frags<LA, TBM, 1>(stage_a(t), rbA + 32 * (i + 1), lane, next);
+          if (i == LAST) {
+            // the last fragments are on their way: this stage is free once every wavefront is here,
+            // and K tile t + 1 has landed once all but the newest loads have
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"(NEWER) : "memory");
+            barrier_lds();
+            issue_a(t + NA);
+            issue_b(t + NB);
+          }
+          if (i < LIVE) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+              for (int j = 0; j < WTN; ++j) Op::mma(acc[i][j], fb[j][s], fa[0][s]);
+          }
+        }
+        if (LIVE > 0) {
+          read_frags<LA, TBM, 1>(stage_a(t + 1), rbA, lane, next);
+          read_frags<LB, TB, WTN>(stage_b(t + 1), rbB, lane, fb);  // (past the end: zeros, not used)
+        }
+      }
+    };
+    const int64_t left = (m_end - m0 - rbA + 31) / 32;
+    if constexpr (GRAD) k_loop(std::integral_constant<int, WTM>{});
+    else with_live<WTM>(left < WTM ? (int)left : WTM, k_loop);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no LDS DMA outstanding at exit
     barrier_lds();
   }
@@ -176,29 +178,65 @@ __global__ __launch_bounds__(2 * TB) __attribute__((amdgpu_waves_per_eu(2, 2))) 
       v[t] = *(const lds_f32x4*)(wbuf + r * 256 + ((cc ^ (r & 15)) << 4));
     }
     const int64_t m = m0 + rbA + 32 * i + rr, n = n0 + rbB + 4 * cc;
-#pragma unroll
-    for (int t = 0; t < 8; ++t)
-      if (m + 4 * t < m_end && n < p.N) group_store4(p, dbase, m + 4 * t, n, v[t]);
+    group_store_rows(p, dbase, m, m_end, n, v);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 }
 
-template <class Op, int LA, int LB, int TB, bool GRAD>
+// TBM x TB tiles (256 x 256, 128 x 128, 64 x 128); with TBM = TB a group's last one of up to TB / 2 rows is
+// TB / 2 x TB.
+template <class Op, int LA, int LB, int TBM, int TB, bool GRAD>
+__global__ __launch_bounds__(2 * TB) __attribute__((amdgpu_waves_per_eu(2, 2))) void group_pipe_kernel(GroupArgs p) {
+  constexpr int LDS = Ring<TBM, TB>::BYTES;
+  static_assert(LDS >= Ring<TB / 2, TB>::BYTES, "ring of a short tile");
+  __shared__ __attribute__((aligned(1024))) char smem_raw[LDS];
+  lds_char* smem = (lds_char*)smem_raw;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  if constexpr (GRAD) {
+    // (groups one after the other, each spread over the XCDs: with whole groups on an XCD, the one with
+    // the longest group ends last: 8192 rows over 16 experts, 4096 x 4096 515 us, so 385)
+    const int tiles = p.tiles_m * p.tiles_n, g = blockIdx.x / tiles;
+    int tm, tn;
+    grouped_tile<4>(xcd_order(blockIdx.x - g * tiles, tiles), p.tiles_m, p.tiles_n, tm, tn);
+    const GroupRows r = group_rows(p.offsets, g, p.K);
+    pipe_tile_work<Op, LA, LB, TB, TB, true>(p, smem, p.A + r.r0 * p.lda * 2, p.B + r.r0 * p.ldb * 2, r.r1 - r.r0, (int64_t)tm * TB,
+                                             p.M, (int64_t)tn * TB, g * p.strideD, wave, lane);
+  } else {
+    const PipeTile w = pipe_tile<TBM>(p.offsets, p.groups, p.M, p.tiles_n, blockIdx.x, lane);
+    if (w.m0 >= w.r1) return;  // (the whole workgroup)
+    const char* B = p.B + w.g * p.strideB * 2;
+    if (TBM == TB && w.r1 - w.m0 > TB / 2)
+      pipe_tile_work<Op, LA, LB, TB, TB, false>(p, smem, p.A, B, p.K, w.m0, w.r1, (int64_t)w.tn * TB, 0, wave, lane);
+    else
+      pipe_tile_work<Op, LA, LB, TB / 2, TB, false>(p, smem, p.A, B, p.K, w.m0, w.r1, (int64_t)w.tn * TB, 0, wave, lane);
+  }
+}
+
+template <class Op, int LA, int LB, int TBM, int TB, bool GRAD>
 hipError_t launch_one(const GroupArgs& a0, hipStream_t s) {
   GroupArgs a = a0;
-  a.tiles_m = (int)(GRAD ? (a.M + TB - 1) / TB : most_tiles(a.M, a.groups, TB, true));
+  a.tiles_m = (int)(GRAD ? (a.M + TBM - 1) / TBM : most_tiles(a.M, a.groups, TBM, true));
   a.tiles_n = (int)((a.N + TB - 1) / TB);
-  const int64_t blocks = (int64_t)a.tiles_m * a.tiles_n * (GRAD ? a.groups : 1);
+  const int64_t blocks = GRAD ? (int64_t)a.tiles_m * a.tiles_n * a.groups : slice_blocks(a.tiles_m, a.tiles_n);
   if (blocks >= MANY_TILES) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((group_pipe_kernel<Op, LA, LB, TB, GRAD>), dim3((unsigned)blocks), dim3(2 * TB), 0, s, a);
+  hipLaunchKernelGGL((group_pipe_kernel<Op, LA, LB, TBM, TB, GRAD>), dim3((unsigned)blocks), dim3(2 * TB), 0, s, a);
   return hipGetLastError();
 }
 
-template <class Op, int TB>
-hipError_t launch_kinds(int lb, bool grad, const GroupArgs& a, hipStream_t s) {
-  if (grad) return launch_one<Op, LAYOUT_MN, LAYOUT_MN, TB, true>(a, s);
-  return lb == LAYOUT_K ? launch_one<Op, LAYOUT_K, LAYOUT_K, TB, false>(a, s)
-                        : launch_one<Op, LAYOUT_K, LAYOUT_MN, TB, false>(a, s);
+template <class Op, int TBM, int TB>
+hipError_t launch_rows(int lb, const GroupArgs& a, hipStream_t s) {
+  return lb == LAYOUT_K ? launch_one<Op, LAYOUT_K, LAYOUT_K, TBM, TB, false>(a, s)
+                        : launch_one<Op, LAYOUT_K, LAYOUT_MN, TBM, TB, false>(a, s);
+}
+// tile: 256 and 128, square tiles; 64: (rows) 64 x 128
+template <class Op>
+hipError_t launch_op(int lb, bool grad, int tile, const GroupArgs& a, hipStream_t s) {
+  if (grad)
+    return tile == 256 ? launch_one<Op, LAYOUT_MN, LAYOUT_MN, 256, 256, true>(a, s)
+                       : launch_one<Op, LAYOUT_MN, LAYOUT_MN, 128, 128, true>(a, s);
+  return tile == 256   ? launch_rows<Op, 256, 256>(lb, a, s)
+         : tile == 128 ? launch_rows<Op, 128, 128>(lb, a, s)
+                       : launch_rows<Op, 64, 128>(lb, a, s);
 }
 
 }  // namespace gpipe
