@@ -6,37 +6,48 @@
 //   8-bit  D[i][j] = sum_b sa[i][b] sb[b][j] sum_{k in b} A[i][k] B[k][j] + beta C[i][j]
 //                                                        (blocks b of 128 k; also by rows)
 //
-// Tiles of 128, 64 or 32 rows x 128 columns, 4 wavefronts; the loaders of tile_any.hpp
+// Tiles of 128 (16-bit), 64 or 32 rows x 128 columns, 4 wavefronts; the loaders of tile_any.hpp
 // (two K tiles ahead in registers, two stages in LDS).  A K tile of 8-bit values is one
-// block of 128: its codes, widened exactly to bf16, are summed on the bf16 instructions in
-// accumulators of their own, which are then multiplied by the block's two scales and
-// added to the tile's sums, all in binary32.
+// block of 128, whose sum leaves the matrix instructions before it is scaled and added
+// (f8_block_ops.hpp: the 8-bit instruction for a bf16 D, else products widened to bf16).
 //
 // Bound: the general kernels' loop (one barrier per K tile between register-staged
 // tiles), about half the matrix rate of the pipelined kernels.
 #include "experts.hpp"
+#include "f8_block_ops.hpp"
 #include "group_epilogue.hpp"
 #include "group_tiles.hpp"
 #include "tile_any.hpp"
 
 namespace mcg {
 
+// 8-bit operands: Block is f8b::Native or f8b::Wide.
+template <class Block>
+struct OpBlocks {
+  static constexpr int ELEM_BYTES = 1, STEPS = 1;
+};
 template <class Op>
 struct IsScaled {
-  static constexpr bool value = Op::ELEM_BYTES == 1;
+  static constexpr bool value = false;
+  using block_t = void;
+};
+template <class Block>
+struct IsScaled<OpBlocks<Block>> {
+  static constexpr bool value = true;
+  using block_t = Block;
 };
 
 template <class Op, int LA, int LB, int BM, bool GRAD>
-__global__ __launch_bounds__(256, IsScaled<Op>::value && BM > 32 ? 1 : 2) void group_general_kernel(GroupArgs p) {
+__global__ __launch_bounds__(256, 2) void group_general_kernel(GroupArgs p) {
   constexpr int EB = Op::ELEM_BYTES, BN = 128, NT = 256, KE = KT_BYTES / EB;
   constexpr bool SCALED = IsScaled<Op>::value;
   using WG = WaveGrid<BM>;
   constexpr int WTM = WG::WTM, WTN = WG::WTN;
   using GA = TileGeom<EB, LA, BM>;
   using GB = TileGeom<EB, LB, BN>;
-  using RA = FragReader<EB, 16, LA, BM>;
-  using RB = FragReader<EB, 16, LB, BN>;
-  constexpr int STAGE = GA::BYTES + GB::BYTES;
+  using RA = FragReader<EB, SCALED ? 32 : 16, LA, BM>;
+  using RB = FragReader<EB, SCALED ? 32 : 16, LB, BN>;
+  constexpr int STAGE = GA::BYTES + GB::BYTES + (SCALED ? NT * 4 : 0);  // codes, and a scale from each thread
   __shared__ __attribute__((aligned(16))) char smem_raw[2 * STAGE];
   lds_char* smem = (lds_char*)smem_raw;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -90,10 +101,28 @@ __global__ __launch_bounds__(256, IsScaled<Op>::value && BM > 32 ? 1 : 2) void g
     constexpr int SETS = 2;
     typename LdA::Regs ra[SETS];
     typename LdB::Regs rb[SETS];
+    // 8-bit: threads 0 .. 127 load the scales of the tile's columns, the others those of its rows (past
+    // either's end: the last one's), zero for K tiles past the end.
+    typedef __attribute__((address_space(3))) float lds_f32;
+    const global_f32* scale = nullptr;
+    int64_t scale_step = 1;
+    float rs[SETS];
+    if constexpr (SCALED) {
+      if (tid < BN) {
+        const int64_t n = min(n0 + tid, p.N - 1), c = p.blockB == 1 ? n : n / SCALE_BLOCK;
+        scale = (const global_f32*)(sb + (LB == LAYOUT_K ? c * p.ldsb : c));
+        if (LB == LAYOUT_MN) scale_step = p.ldsb;
+      } else {
+        const int64_t m = min(m0 + (tid - BN) % BM, m_end - 1);
+        scale = (const global_f32*)(p.sa + (LA == LAYOUT_K ? m * p.ldsa : m));
+        if (LA == LAYOUT_MN) scale_step = p.ldsa;
+      }
+    }
     auto load_tile = [&](auto set_c, int kt) {
       constexpr int set = decltype(set_c)::value;
       la.load(ra[set], kt, kt < nk);
       lb.load(rb[set], kt, kt < nk);
+      if constexpr (SCALED) rs[set] = kt < nk ? scale[kt * scale_step] : *(const global_f32*)(const float*)load_nothing;
     };
     auto store_tile = [&](auto set_c, int kt) {
       constexpr int set = decltype(set_c)::value;
@@ -102,63 +131,46 @@ __global__ __launch_bounds__(256, IsScaled<Op>::value && BM > 32 ? 1 : 2) void g
       lb.settle(rb[set], kt);
       la.store(ra[set], st);
       lb.store(rb[set], st + GA::BYTES);
+      if constexpr (SCALED) *(lds_f32*)(st + GA::BYTES + GB::BYTES + 4 * tid) = rs[set];
     };
     using ACC = frag::Acc<frag::ACC_16x16>;
     const int am = ACC::coord(lane, 0).j, an = ACC::coord(lane, 0).i;  // row and first of 4 columns in a block
     auto step = [&](auto set_c, int kt) {
       constexpr int set = decltype(set_c)::value;
       const lds_char* cur = smem + (set & 1) * STAGE;
-      // scales of K tile kt (zero past the end, where the codes are zero)
-      float sa[WTM], sc[WTN][4];
-      if constexpr (SCALED) {
-        const global_f32* psa = (const global_f32*)p.sa;
-        const global_f32* psb = (const global_f32*)sb;
-        const int64_t b = min(kt, nk - 1);
-#pragma unroll
-        for (int i = 0; i < WTM; ++i) {
-          const int64_t m = min(m0 + rm + 16 * i + am, m_end - 1);
-          sa[i] = psa[LA == LAYOUT_K ? m * p.ldsa + b : b * p.ldsa + m];
-        }
-#pragma unroll
-        for (int j = 0; j < WTN; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int64_t n = min(n0 + rn + 16 * j + an + e, p.N - 1), c = p.blockB == 1 ? n : n / SCALE_BLOCK;
-            sc[j][e] = psb[LB == LAYOUT_K ? c * p.ldsb + b : b * p.ldsb + c];
-          }
-      }
       store_tile(std::integral_constant<int, (set + 1) % SETS>{}, kt + 1);
       load_tile(std::integral_constant<int, (set + 1) % SETS>{}, kt + 1 + SETS);
-      f32x4 part[SCALED ? WTM : 1][SCALED ? WTN : 1];
       if constexpr (SCALED) {
+        using Block = typename IsScaled<Op>::block_t;
+        const lds_f32* ssb = (const lds_f32*)(cur + GA::BYTES + GB::BYTES);
+        const lds_f32* ssa = ssb + BN;
+        typename Block::frag_t fb[WTN];
 #pragma unroll
-        for (int i = 0; i < WTM; ++i)
+        for (int j = 0; j < WTN; ++j) fb[j] = Block::b(RB::read(cur + GA::BYTES, rn + j * 16, 0, lane));
 #pragma unroll
-          for (int j = 0; j < WTN; ++j) part[i][j] = f32x4{0, 0, 0, 0};
-      }
-#pragma unroll
-      for (int s = 0; s < Op::STEPS; ++s) {
-        typename Op::frag_t fa[WTM], fb[WTN];
-#pragma unroll
-        for (int i = 0; i < WTM; ++i) fa[i] = Op::template frag_a<RA>(cur, rm + i * 16, s, lane);
-#pragma unroll
-        for (int j = 0; j < WTN; ++j) fb[j] = Op::template frag_b<RB>(cur + GA::BYTES, rn + j * 16, s, lane);
-#pragma unroll
-        for (int i = 0; i < WTM; ++i)
+        for (int i = 0; i < WTM; ++i) {
+          const auto fa = Block::a(RA::read(cur, rm + i * 16, 0, lane));
+          const float sa = ssa[rm + 16 * i + am];
 #pragma unroll
           for (int j = 0; j < WTN; ++j) {
-            if constexpr (SCALED) part[i][j] = Op::mma(fb[j], fa[i], part[i][j]);
-            else acc[i][j] = Op::mma(fb[j], fa[i], acc[i][j]);
+            typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+            const f32x4 part = Block::block(fb[j], fa), sc = *(const lds_f32x4*)(ssb + rn + 16 * j + an);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(part[e], sa * sc[e], acc[i][j][e]);
           }
-      }
-      if constexpr (SCALED) {
-        if (kt < nk) {  // (past the end a scale that is no number would leave its mark)
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < Op::STEPS; ++s) {
+          i32x4 fa[WTM], fb[WTN];
+#pragma unroll
+          for (int i = 0; i < WTM; ++i) fa[i] = RA::read(cur, rm + i * 16, s, lane);
+#pragma unroll
+          for (int j = 0; j < WTN; ++j) fb[j] = RB::read(cur + GA::BYTES, rn + j * 16, s, lane);
 #pragma unroll
           for (int i = 0; i < WTM; ++i)
 #pragma unroll
-            for (int j = 0; j < WTN; ++j)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(part[i][j][e], sa[i] * sc[j][e], acc[i][j][e]);
+            for (int j = 0; j < WTN; ++j) acc[i][j] = Op::mma(fb[j], fa[i], acc[i][j]);
         }
       }
       barrier_tiles();
@@ -259,20 +271,29 @@ static hipError_t launch_16(int lb, bool grad, const GroupArgs& a, int tile, hip
   return lb == LAYOUT_K ? launch_rows<Op, LAYOUT_K, LAYOUT_K, false>(a, tile, s)
                         : launch_rows<Op, LAYOUT_K, LAYOUT_MN, false>(a, tile, s);
 }
+// (8-bit tiles of 128 rows spill over 100 registers, or leave a compute unit with one workgroup: 5658 x 1472 x
+// 4672 from rows of odd lengths 396 us, 172 in tiles of 64 rows)
+template <class Op, int LA, int LB>
+static hipError_t launch_rows8(const GroupArgs& a, int tile, hipStream_t s) {
+  return tile == 32 ? launch_one<Op, LA, LB, 32, false>(a, s) : launch_one<Op, LA, LB, 64, false>(a, s);
+}
 template <class Op>
 static hipError_t launch_8(int la, int lb, const GroupArgs& a, int tile, hipStream_t s) {
   if (la == LAYOUT_K)
-    return lb == LAYOUT_K ? launch_rows<Op, LAYOUT_K, LAYOUT_K, false>(a, tile, s)
-                          : launch_rows<Op, LAYOUT_K, LAYOUT_MN, false>(a, tile, s);
-  return lb == LAYOUT_K ? launch_rows<Op, LAYOUT_MN, LAYOUT_K, false>(a, tile, s)
-                        : launch_rows<Op, LAYOUT_MN, LAYOUT_MN, false>(a, tile, s);
+    return lb == LAYOUT_K ? launch_rows8<Op, LAYOUT_K, LAYOUT_K>(a, tile, s)
+                          : launch_rows8<Op, LAYOUT_K, LAYOUT_MN>(a, tile, s);
+  return lb == LAYOUT_K ? launch_rows8<Op, LAYOUT_MN, LAYOUT_K>(a, tile, s)
+                        : launch_rows8<Op, LAYOUT_MN, LAYOUT_MN>(a, tile, s);
 }
 
 hipError_t launch_group_general(int dt, int la, int lb, bool grad, const GroupArgs& a, int tile, hipStream_t s) {
+  using f8b::Native;
+  using f8b::Wide;
   if (dt == DT_BF16) return launch_16<OpBF16>(lb, grad, a, tile, s);
   if (dt == DT_F16) return launch_16<OpF16>(lb, grad, a, tile, s);
-  if (dt == DT_E4M3) return launch_8<OpF8W<0, 0>>(la, lb, a, tile, s);
-  return launch_8<OpF8W<1, 0>>(la, lb, a, tile, s);
+  const bool wide = a.out != OUT_BF16;
+  if (dt == DT_E4M3) return wide ? launch_8<OpBlocks<Wide<0>>>(la, lb, a, tile, s) : launch_8<OpBlocks<Native<0>>>(la, lb, a, tile, s);
+  return wide ? launch_8<OpBlocks<Wide<1>>>(la, lb, a, tile, s) : launch_8<OpBlocks<Native<1>>>(la, lb, a, tile, s);
 }
 
 hipError_t launch_group_tiny(int dt, int la, int lb, bool grad, const GroupArgs& a, hipStream_t s) {

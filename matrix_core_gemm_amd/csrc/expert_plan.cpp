@@ -10,8 +10,11 @@ namespace mcg {
 namespace {
 int64_t cdiv(int64_t x, int64_t y) { return (x + y - 1) / y; }
 int64_t elem_bytes(int dt) { return dt == MCG_BF16 || dt == MCG_F16 ? 2 : 1; }
-// Rows of at least one 16-byte load, as the general kernels' loaders need them.
-bool rows_ok(int64_t eb, int64_t K, int64_t mn, int layout) { return (layout == MCG_K_CONTIG ? K : mn) * eb >= 16; }
+// An operand of at least one 16-byte load, as the general kernels' loaders need it.
+bool load_ok(int64_t eb, int64_t K, int64_t mn, int64_t ld, int layout) {
+  const int64_t rows = layout == MCG_K_CONTIG ? mn : K, cols = layout == MCG_K_CONTIG ? K : mn;
+  return ((rows - 1) * ld + cols) * eb >= 16;
+}
 bool aligned_to(const void* p, int64_t a) { return (uintptr_t)p % (uintptr_t)a == 0; }
 constexpr int64_t LIM = (int64_t)1 << 31;  // buffer windows and offsets stay below it
 
@@ -32,68 +35,110 @@ bool f8_pipe_ok(const GroupArgs& a, int la, int lb) {
          4 * (lb == MCG_K_CONTIG ? 256 : kb) * a.ldsb < LIM;
 }
 
-// Rows of the general kernels' tiles (see general_rows in tile_any.hpp).
-int general_tile_rows(int64_t rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+
+// A choice and its modelled time.
+struct Timed {
+  GroupPlan plan;
+  double us;
+};
 
 // One round of a pipelined kernel's tiles: kt_us for each K tile of 128 bytes and fixed_us, most of it
-// the epilogue.  Of the tiles with 128 columns a compute unit holds two: `alone` where it has one.
+// the epilogue.  Of the tiles with 128 columns a compute unit holds two: `alone` where it has one, a
+// quarter less where most units have none.
 struct TileTime {
   int tile;
   double kt_us, alone_us, fixed_us;
 };
 constexpr TileTime TIMES_16[] = {{256, 1.45, 1.45, 12.0}, {128, 1.0, 0.62, 8.0}, {64, 0.75, 0.45, 6.0}};
-constexpr TileTime TIMES_F8[] = {{256, 1.85, 1.85, 12.0}, {128, 1.2, 0.7, 8.0}, {64, 0.85, 0.5, 6.0}};
+constexpr TileTime TIMES_F8[] = {{256, 1.85, 1.85, 12.0}, {128, 1.2, 0.7, 8.0}, {64, 0.85, 0.5, 5.0}};
 constexpr TileTime TIMES_WIDE[] = {{128, 2.0, 1.2, 8.0}, {64, 1.3, 0.8, 6.0}};
 
 // tiles(t): tiles of t rows; nk K tiles each.
 template <int N, class F>
-GroupPlan best_tile(const TileTime (&times)[N], int64_t nk, int64_t cols, int num_cu, int least, F tiles) {
-  GroupPlan best{KERNEL_GENERAL, 0};
-  double best_us = 0.0;
+Timed best_tile(const TileTime (&times)[N], int64_t nk, int64_t cols, int num_cu, int least, F tiles) {
+  Timed best{{KERNEL_GENERAL, 0}, 0.0};
   for (const TileTime& t : times) {
     if (t.tile < least) continue;
     const int64_t n = tiles(t.tile) * cdiv(cols, t.tile == 256 ? 256 : 128);
     const int64_t at_once = t.tile == 256 ? num_cu : 2 * (int64_t)num_cu;
-    const double us = n <= num_cu ? t.alone_us * nk + t.fixed_us : cdiv(n, at_once) * (t.kt_us * nk + t.fixed_us);
-    if (best.tile == 0 || us < best_us) {
-      best = {t.tile == 256 ? KERNEL_FAST : t.tile == 128 ? KERNEL_MID : KERNEL_HALF, t.tile};
-      best_us = us;
-    }
+    const double us = n <= num_cu ? t.alone_us * (0.75 + 0.25 * (double)n / num_cu) * nk + t.fixed_us
+                                  : (double)cdiv(n, at_once) * (t.kt_us * nk + t.fixed_us);
+    if (best.plan.tile == 0 || us < best.us)
+      best = {{t.tile == 256 ? KERNEL_FAST : t.tile == 128 ? KERNEL_MID : KERNEL_HALF, t.tile}, us};
   }
   return best;
 }
-// Tiles that the rows of groups of unknown sizes take: half a tile of each group's last one is empty.
+// Tiles that the rows of groups of unknown sizes take: half a tile of each group's last one is empty, and
+// where there are few rows a quarter of the groups.
 int64_t likely_tiles(const GroupArgs& a, int64_t tile) {
   if (!a.offsets || a.groups == 1) return cdiv(a.M, tile);
-  return cdiv(a.M, tile) + std::min<int64_t>(a.groups, a.M) / 2;
+  const int64_t some = std::min<int64_t>(a.groups, a.M);
+  return std::max(cdiv(a.M, tile) + some / 2, some * 3 / 4);
+}
+// Rows of the general kernels' tiles: the most that leave a workgroup for each compute unit (8-bit 276 x
+// 5056 x 3776 from rows of odd lengths: 200 workgroups of 64 rows 76 us, 360 of 32 57; 2000 x 2001 x 2003: 512
+// of 64 rows 39 us, 32 rows 57; bf16 2000 rows over 9 groups, 1003 x 1501: 168 of 128 rows 43 us, 288 of 64 34).
+template <class F>
+GroupPlan general_plan(int most, int64_t cols, int num_cu, F tiles) {
+  for (int t = most; t > 32; t /= 2)
+    if (tiles(t) * cdiv(cols, 128) >= num_cu) return {KERNEL_GENERAL, t};
+  return {KERNEL_GENERAL, 32};
+}
+// The kernel for few rows: 28 KB a us and compute unit (see expert_rows.hip), and 0.7 us for a
+// workgroup (10 rows over 28 groups, 6208 x 128: 20 us in workgroups of 32 columns, 8.6 in tiles of 64 x 128).
+Timed best_few_rows(const GroupArgs& a, int64_t eb, int num_cu) {
+  Timed best{{KERNEL_GENERAL, 0}, 0.0};
+  for (int tile = 16; tile <= 64; tile *= 2) {
+    const double per_cu = (double)likely_tiles(a, tile) * (double)cdiv(a.N, 32) / num_cu;
+    const double us = 6.0 + (per_cu < 1.0 ? 1.0 : per_cu) * (0.7 + (32 + tile) * (double)(a.K * eb) / 28e3);
+    if (best.plan.tile == 0 || us < best.us) best = {{KERNEL_ROWS, tile}, us};
+  }
+  return best;
 }
 }  // namespace
 
 GroupPlan plan_grouped(int dt, int la, int lb, const GroupArgs& a, int num_cu) {
   const int64_t eb = elem_bytes(dt);
-  if (a.K == 0 || !rows_ok(eb, a.K, a.M, la) || !rows_ok(eb, a.K, a.N, lb)) return {KERNEL_TINY, 1};
+  if (a.K == 0 || !load_ok(eb, a.K, a.M, a.lda, la) || !load_ok(eb, a.K, a.N, a.ldb, lb)) return {KERNEL_TINY, 1};
   const int64_t nk = cdiv(a.K * eb, 128), rows = a.M / a.groups;
+  const bool chunks = chunks_ok(eb, a, la, lb, 3);
+  const bool pipe = chunks && (eb == 2 || f8_pipe_ok(a, la, lb));
+  const bool few = chunks && rows <= 64 && la == MCG_K_CONTIG && lb == MCG_K_CONTIG &&
+                   (eb == 2 || (a.blockB == SCALE_BLOCK && 4 * 256 * a.ldsa < LIM));
   auto tiles = [&](int t) { return likely_tiles(a, t); };
-  if (rows > 32 && eb == 2 && chunks_ok(2, a, la, lb, 3)) return best_tile(TIMES_16, nk, a.N, num_cu, 64, tiles);
-  if (rows > 32 && eb == 1 && f8_pipe_ok(a, la, lb))
-    return a.out == OUT_BF16 ? best_tile(TIMES_F8, nk, a.N, num_cu, 64, tiles) : best_tile(TIMES_WIDE, nk, a.N, num_cu, 64, tiles);
-  return {KERNEL_GENERAL, general_tile_rows(rows)};
+  Timed best{general_plan(eb == 2 ? 128 : 64, a.N, num_cu, tiles), 0.0};
+  if (pipe) {
+    best = eb == 2              ? best_tile(TIMES_16, nk, a.N, num_cu, 64, tiles)
+           : a.out == OUT_BF16 ? best_tile(TIMES_F8, nk, a.N, num_cu, 64, tiles)
+                               : best_tile(TIMES_WIDE, nk, a.N, num_cu, 64, tiles);
+    // (the weights of four groups in five come from HBM, at 4.3 TB/s in these kernels' tiles of few rows)
+    const double weights_us = 5.0 + 0.8 * (double)std::min<int64_t>(a.groups, a.M) * (double)(a.N * a.K * eb) / 4.3e6;
+    best.us = std::max(best.us, weights_us);
+  }
+  if (few) {
+    const Timed t = best_few_rows(a, eb, num_cu);
+    if (best.plan.kernel == KERNEL_GENERAL || t.us < best.us) best = t;
+  }
+  return best.plan;
 }
 
 GroupPlan plan_grouped_grad(int dt, const GroupArgs& a, int num_cu) {
   const int64_t eb = elem_bytes(dt);
+  // (a group may be one row, which is then the operand)
   if (a.K == 0 || a.M * eb < 16 || a.N * eb < 16) return {KERNEL_TINY, 1};
+  auto tiles = [&](int t) { return a.groups * cdiv(a.M, t); };
   if (chunks_ok(2, a, MCG_MN_CONTIG, MCG_MN_CONTIG, 3) && a.M >= 64 && a.N >= 64)
-    return best_tile(TIMES_16, cdiv(a.K * eb, 128 * a.groups), a.N, num_cu, 128, [&](int t) { return a.groups * cdiv(a.M, t); });
-  return {KERNEL_GENERAL, general_tile_rows(a.M)};
+    return best_tile(TIMES_16, cdiv(a.K * eb, 128 * a.groups), a.N, num_cu, 128, tiles).plan;
+  return general_plan(128, a.N, num_cu, tiles);
 }
 
 hipError_t launch_grouped(int dt, int la, int lb, const GroupArgs& a, int num_cu, hipStream_t s) {
   const GroupPlan p = plan_grouped(dt, la, lb, a, num_cu);
   if (p.kernel == KERNEL_TINY) return launch_group_tiny(dt, la, lb, false, a, s);
   if (p.kernel == KERNEL_GENERAL) return launch_group_general(dt, la, lb, false, a, p.tile, s);
-  if (elem_bytes(dt) == 2) return launch_group_pipe(dt, lb, false, p.tile, a, s);
   const bool wide = a.out != OUT_BF16;
+  if (p.kernel == KERNEL_ROWS) return launch_few_rows(dt, p.tile, wide, a, s);
+  if (elem_bytes(dt) == 2) return launch_group_pipe(dt, lb, false, p.tile, a, s);
   if (p.tile == 256) return launch_f8_blocks_256(dt, la, lb, a, s);
   return p.tile == 128 ? launch_f8_blocks_128(dt, la, lb, wide, a, s) : launch_f8_blocks_64(dt, la, lb, wide, a, s);
 }
