@@ -178,7 +178,10 @@ static hipError_t launch_one(const GroupArgs& a0, hipStream_t s) {
 }
 template <class Op>
 static hipError_t launch_op(int rows, const GroupArgs& a, hipStream_t s) {
-  return rows == 16 ? launch_one<Op, 1, 4>(a, s) : rows == 32 ? launch_one<Op, 2, 4>(a, s) : launch_one<Op, 4, 2>(a, s);
+  if (rows == 16) return launch_one<Op, 1, 4>(a, s);
+  if constexpr (Op::EB == 1)
+    if (rows == 64) return launch_one<Op, 4, 2>(a, s);
+  return launch_one<Op, 2, 4>(a, s);
 }
 
 }  // namespace few

@@ -66,7 +66,7 @@ hipError_t launch_f8_blocks_64(int dtA, int la, int lb, bool wide, const GroupAr
 // tiles.
 hipError_t launch_group_pipe(int dt, int lb, bool grad, int tile, const GroupArgs& a, hipStream_t s);
 
-// Few rows of K-contiguous operands (expert_rows.hip): tiles of 16, 32 or 64 rows.
+// Few rows of K-contiguous operands (expert_rows.hip): tiles of 16, 32 or (8-bit) 64 rows.
 hipError_t launch_few_rows(int dt, int rows, bool wide, const GroupArgs& a, hipStream_t s);
 
 // The choice of a kernel, and its launch (expert_plan.cpp).

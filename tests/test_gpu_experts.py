@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+import experts_cases as cases
 import experts_ref as ref
 from experts_ref import BLOCK, DT, F8, KINDS, cdiv
 from gpu_util import need_gpu, say
@@ -404,6 +405,95 @@ def test_gemm_grouped_f8_blocks_of_larger_sizes(lb, shape):
     sizes, N, K = shape
     for to, dtD in (("e4m3", "bf16"), ("e5m2", "f32"), ("e4m3", "f16")):
         check_grouped8(mcg, to, lb, dtD, sizes, N, K, lead=5, tail=70)
+
+
+# ------------------------------------------------------------- every form
+@pytest.mark.parametrize("name", list(cases.GROUPED))
+def test_every_form_of_gemm_grouped(name):
+    mcg = need_gpu()
+    case = cases.GROUPED[name]
+    dt, dtD, lb, sizes, N, K, pad, kernel, tile = case
+    G, M, lda, ldb, strideB = cases.operands_of_grouped(case)
+    say(f"{name}: {dt} {dtD} {lb} {sizes} {N} x {K}")
+    a, b, off = ref.rand(1, M, K).to(DT[dt]), (ref.rand(2, G, K, N) * K ** -0.5).to(DT[dt]), ref.offsets_of(sizes)
+    A, B, D = put(a, pad), put3(b if lb == "mn_contig" else b.transpose(1, 2).contiguous(), pad), buf(M, N, DT[dtD], pad)
+    assert (ld(A), ld(B), B.stride(0)) == (lda, ldb, strideB)
+    assert mcg.grouped_path(dt, "k_contig", lb, G, M, N, K, A, lda, B, ldb, strideB, 128, dtD) == (kernel, tile)
+    outs = []
+    for _ in range(2):  # the same bits again
+        D.fill_(float("nan"))
+        mcg.gemm_grouped(dt, lb, G, M, N, K, off.cuda(), A, lda, B, ldb, strideB, D, ld(D), dtD)
+        guards_hold(D)
+        outs.append(D.cpu())
+    assert torch.equal(outs[0], outs[1])
+    d, mag = ref.grouped(a, b.double(), off)
+    within(outs[0], d, ref.tol_16(d, mag, K, dtD), name)
+
+
+@pytest.mark.parametrize("name", list(cases.GRAD))
+def test_every_form_of_gemm_grouped_grad(name):
+    mcg = need_gpu()
+    dt, dtD, sizes, M, N, pad, kernel, tile = cases.GRAD[name]
+    K, G = sum(sizes), len(sizes)
+    say(f"{name}: {dt} {dtD} {sizes} {M} x {N}")
+    a, b, off = ref.rand(1, K, M).to(DT[dt]), ref.rand(2, K, N).to(DT[dt]), ref.offsets_of(sizes)
+    c = ref.rand(3, G, M, N).to(DT[dtD])
+    A, B, C, D = put(a, pad), put(b, pad), put3(c, pad), put3(torch.zeros(G, M, N).to(DT[dtD]), pad)
+    assert mcg.grouped_grad_path(dt, G, M, N, K, A, ld(A), B, ld(B), dtD) == (kernel, tile)
+    d, mag = ref.grouped_grad(a, b, off, c, 0.5)
+    mag = mag + 0.5 * c.double().abs()
+    outs = []
+    for _ in range(2):
+        mcg.gemm_grouped_grad(dt, G, M, N, K, off.cuda(), A, ld(A), B, ld(B), C, D, ld(D), D.stride(0), dtD, 0.5)
+        guards_hold(D)
+        outs.append(D.cpu())
+    assert torch.equal(outs[0], outs[1])
+    within(outs[0], d, ref.tol_16(d, mag, max(sizes), dtD), name)
+
+
+@pytest.mark.parametrize("name", list(cases.F8))
+def test_every_form_of_gemm_f8_blocks(name):
+    """With C, and over a group of all rows too where the product by group has the kind."""
+    mcg = need_gpu()
+    to, dtD, la, lb, bb, M, N, K, pad, kernel, tile = cases.F8[name]
+    say(f"{name}: {to} {dtD} {la} {lb} {bb} {M} x {N} x {K}")
+    qa, sa, a = f8_operand(1, la, M, K, to, 1)
+    qb, sb, b = f8_operand(2, lb, N, K, "e4m3", bb, K ** -0.5)
+    c = ref.rand(3, M, N).to(DT[dtD])
+    A, B, SA, SB, C, D = put(qa, pad), put(qb, pad), put(sa), put(sb), put(c, pad), buf(M, N, DT[dtD], pad)
+    assert mcg.grouped_path(to, la, lb, 0, M, N, K, A, ld(A), B, ld(B), 0, bb, dtD) == (kernel, tile)
+    d, mag = a @ b.T, a.abs() @ b.abs().T
+    outs = []
+    for _ in range(2):
+        mcg.gemm_f8_blocks(to, "e4m3", la, lb, bb, M, N, K, A, ld(A), SA, ld(SA), B, ld(B), SB, ld(SB), C, D, ld(D), dtD, 0.5)
+        guards_hold(D)
+        outs.append(D.cpu())
+    assert torch.equal(outs[0], outs[1])
+    dc, magc = d + 0.5 * c.double(), mag + 0.5 * c.double().abs()
+    within(outs[0], dc, ref.tol_f8(dc, magc, K, dtD), name)
+    if la == "k_contig" and bb == 128:
+        off = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+        mcg.gemm_grouped_f8_blocks(to, "e4m3", lb, 1, M, N, K, off, A, ld(A), SA, ld(SA), B, ld(B), 0, SB, ld(SB), 0, D, ld(D), dtD)
+        guards_hold(D)
+        within(D, d, ref.tol_f8(d, mag, K, dtD), name + " by group")
+
+
+def test_native_sums_cost_a_tenth_of_a_bf16_rounding():
+    """What the documents say of the 8-bit instructions: the 2-norm of their error is below
+    2^-12 of D's (measured in binary32 through a bf16 D's distance from the exact product)."""
+    mcg = need_gpu()
+    M, N, K = 256, 512, 4096
+    qa, sa, a = f8_operand(1, "k_contig", M, K, "e4m3", 1)
+    qb, sb, b = f8_operand(2, "k_contig", N, K, "e4m3", 128, K ** -0.5)
+    D, E = buf(M, N, torch.bfloat16), buf(M, N, torch.float32)
+    for out, dtD in ((D, "bf16"), (E, "f32")):
+        mcg.gemm_f8_blocks("e4m3", "e4m3", 0, 0, 128, M, N, K, put(qa), K, put(sa), 32, put(qb), K, put(sb), 32, None, out, N, dtD)
+    torch.cuda.synchronize()
+    d = a @ b.T
+    rel = lambda x: float((x - d).norm() / d.norm())
+    rounded = rel(d.bfloat16().double())
+    assert rel(E.cpu().double()) < 2.0 ** -20
+    assert rel(D.cpu().double()) ** 2 - rounded ** 2 < (2.0 ** -12) ** 2, (rel(D.cpu().double()), rounded)
 
 
 # ------------------------------------------------- offsets that are not valid
