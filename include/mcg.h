@@ -480,10 +480,11 @@ int64_t mcg_grad_i8_workspace_bytes(int dtypeA, int layoutA, int64_t M, int64_t 
  * belong to none: they are not read as operands, and outputs there stay as they were.
  * (Offsets that leave the range or decrease are read as the nearest that do not: no
  * access leaves the operands, and the outputs are those of some such groups.)  At most
- * 65535 groups.
+ * 65535 groups, and fewer than 2^23 - 64 tiles of 128 x 128 outputs (64 x 128 of 8-bit
+ * operands), counting each group's last one whole (MCG_ERR_INVALID_SIZE otherwise).
  *
  * Matrices are row-major with a leading dimension in elements, at any alignment of their
- * elements.  All calls are deterministic, need no workspace and may overlap.
+ * elements.  All calls are deterministic, need no workspace and may run at the same time.
  * ---------------------------------------------------------------------------
  *
  * quantize_blocks / dequantize_blocks -- a matrix in 8-bit floats with a scale for each
@@ -495,7 +496,7 @@ int64_t mcg_grad_i8_workspace_bytes(int dtypeA, int layoutA, int64_t M, int64_t 
  * dtype, dtypeD : MCG_BF16, MCG_F16 or MCG_F32.   dtypeQ: MCG_FP8_E4M3 or MCG_FP8_E5M2.
  * blockM, blockN: 1 x 128 (128 values of a row), 128 x 1 (of a column) or 128 x 128
  *                 (MCG_ERR_INVALID_VALUE otherwise).  The last block of a row or column
- *                 may be smaller.
+ *                 may be smaller.  N is at most 128 (2^24 - 1).
  * scale, lds    : one binary32 value per block, ceil(M / blockM) x ceil(N / blockN).
  * L x is rounded to binary32 (exact for 16-bit x), and so is its quotient by max|x|
  * before it is rounded to 8 bits: of 16-bit x the codes are those of the exact quotient.

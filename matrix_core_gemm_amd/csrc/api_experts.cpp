@@ -9,6 +9,7 @@ namespace {
 
 constexpr int64_t MAX_GROUPS = 65535;  // (a grid's second dimension)
 constexpr int64_t BLOCK = mcg::SCALE_BLOCK;
+constexpr int64_t MAX_COLUMN_BLOCKS = (1 << 24) - 1;  // (a grid holds less than 2^32 threads along a dimension: 256 for each)
 
 bool sizes_ok(int64_t a, int64_t b, int64_t c) {
   return a >= 0 && b >= 0 && c >= 0 && a <= INT32_MAX && b <= INT32_MAX && c <= INT32_MAX;
@@ -18,6 +19,12 @@ int64_t cdiv(int64_t x, int64_t y) { return (x + y - 1) / y; }
 bool f16_type(int dt) { return dt == MCG_BF16 || dt == MCG_F16; }
 bool f8_type(int dt) { return dt == MCG_FP8_E4M3 || dt == MCG_FP8_E5M2; }
 bool block_ok(int bm, int bn) { return (bm == 1 && bn == BLOCK) || (bm == BLOCK && (bn == 1 || bn == BLOCK)); }
+
+// Tiles of G groups of M rows, or (grouped false) of one product, by N columns, 16- or 8-bit operands.
+bool tiles_ok(int eb, int64_t M, int64_t G, int64_t N, bool grouped) {
+  return mcg::tiles_fit(mcg::most_tiles(M, G, mcg::general_rows(eb), grouped), N, 128);
+}
+bool grad_tiles_ok(int64_t G, int64_t M, int64_t N) { return mcg::tiles_fit(G * cdiv(M, mcg::general_rows(2)), N, 128); }
 
 int out_format(int dtypeD) {
   return dtypeD == MCG_BF16 ? mcg::OUT_BF16 : dtypeD == MCG_F16 ? mcg::OUT_F16 : mcg::OUT_32;
@@ -58,7 +65,7 @@ int mcg_validate_quantize_blocks(int dtype, int dtypeQ, int blockM, int blockN, 
                                  int64_t ldx, const void* Q, int64_t ldq, const void* scale, int64_t lds) {
   if (!float_out(dtype) || !f8_type(dtypeQ)) return MCG_ERR_UNSUPPORTED_DTYPE;
   if (!block_ok(blockM, blockN)) return MCG_ERR_INVALID_VALUE;
-  if (!sizes_ok(M, N, 0)) return MCG_ERR_INVALID_SIZE;
+  if (!sizes_ok(M, N, 0) || cdiv(N, BLOCK) > MAX_COLUMN_BLOCKS) return MCG_ERR_INVALID_SIZE;
   if (M == 0 || N == 0) return MCG_SUCCESS;
   if (!X || !Q || !scale) return MCG_ERR_NULL_POINTER;
   if (!ld_ok(ldx, N) || !ld_ok(ldq, N) || !ld_ok(lds, cdiv(N, blockN))) return MCG_ERR_INVALID_LD;
@@ -81,7 +88,7 @@ int mcg_validate_dequantize_blocks(int dtypeQ, int dtypeD, int blockM, int block
                                    int64_t ldd) {
   if (!f8_type(dtypeQ) || !float_out(dtypeD)) return MCG_ERR_UNSUPPORTED_DTYPE;
   if (!block_ok(blockM, blockN)) return MCG_ERR_INVALID_VALUE;
-  if (!sizes_ok(M, N, 0)) return MCG_ERR_INVALID_SIZE;
+  if (!sizes_ok(M, N, 0) || cdiv(N, BLOCK) > MAX_COLUMN_BLOCKS) return MCG_ERR_INVALID_SIZE;
   if (M == 0 || N == 0) return MCG_SUCCESS;
   if (!Q || !scale || !D) return MCG_ERR_NULL_POINTER;
   if (!ld_ok(ldq, N) || !ld_ok(ldd, N) || !ld_ok(lds, cdiv(N, blockN))) return MCG_ERR_INVALID_LD;
@@ -107,6 +114,7 @@ int mcg_validate_grouped(int dtype, int layoutB, int64_t G, int64_t M, int64_t N
     return MCG_ERR_UNSUPPORTED_DTYPE;
   if (!sizes_ok(M, N, K) || G < 0 || G > MAX_GROUPS || strideB < 0) return MCG_ERR_INVALID_SIZE;
   if (G == 0 || M == 0 || N == 0) return MCG_SUCCESS;
+  if (!tiles_ok(2, M, G, N, true)) return MCG_ERR_INVALID_SIZE;
   if (!offsets || !D || (K > 0 && (!A || !B))) return MCG_ERR_NULL_POINTER;
   if (!ld_ok(lda, K) || !ld_ok(ldb, layoutB == MCG_K_CONTIG ? K : N) || !ld_ok(ldd, N)) return MCG_ERR_INVALID_LD;
   if (!aligned_to(offsets, 4) || !aligned_to(A, 2) || !aligned_to(B, 2) || !aligned_to(D, elem_bytes(dtypeD)))
@@ -135,6 +143,7 @@ int mcg_validate_grouped_grad(int dtype, int64_t G, int64_t M, int64_t N, int64_
   if (!sizes_ok(M, N, K) || G < 0 || G > MAX_GROUPS) return MCG_ERR_INVALID_SIZE;
   if (!std::isfinite((float)beta)) return MCG_ERR_INVALID_VALUE;
   if (G == 0 || M == 0 || N == 0) return MCG_SUCCESS;
+  if (!grad_tiles_ok(G, M, N)) return MCG_ERR_INVALID_SIZE;
   if (!D || (K > 0 && (!offsets || !A || !B)) || (beta != 0.0 && !C)) return MCG_ERR_NULL_POINTER;
   if (!ld_ok(lda, M) || !ld_ok(ldb, N) || !ld_ok(ldd, N) || (G > 1 && strideD < (M - 1) * ldd + N))
     return MCG_ERR_INVALID_LD;
@@ -169,6 +178,7 @@ int mcg_validate_f8_blocks(int dtypeA, int dtypeB, int layoutA, int layoutB, int
   if ((blockB != 1 && blockB != BLOCK) || !std::isfinite((float)beta)) return MCG_ERR_INVALID_VALUE;
   if (!sizes_ok(M, N, K)) return MCG_ERR_INVALID_SIZE;
   if (M == 0 || N == 0) return MCG_SUCCESS;
+  if (!tiles_ok(1, M, 1, N, false)) return MCG_ERR_INVALID_SIZE;
   if (!D || (K > 0 && (!A || !B || !scaleA || !scaleB)) || (beta != 0.0 && !C)) return MCG_ERR_NULL_POINTER;
   const int64_t kb = cdiv(K, BLOCK), nb = cdiv(N, blockB);
   if (!ld_ok(lda, layoutA == MCG_K_CONTIG ? K : M) || !ld_ok(ldb, layoutB == MCG_K_CONTIG ? K : N) || !ld_ok(ldd, N) ||
@@ -206,6 +216,7 @@ int mcg_validate_grouped_f8_blocks(int dtypeA, int dtypeB, int layoutB, int64_t 
     return MCG_ERR_UNSUPPORTED_DTYPE;
   if (!sizes_ok(M, N, K) || G < 0 || G > MAX_GROUPS || strideB < 0 || strideSB < 0) return MCG_ERR_INVALID_SIZE;
   if (G == 0 || M == 0 || N == 0) return MCG_SUCCESS;
+  if (!tiles_ok(1, M, G, N, true)) return MCG_ERR_INVALID_SIZE;
   if (!offsets || !D || (K > 0 && (!A || !B || !scaleA || !scaleB))) return MCG_ERR_NULL_POINTER;
   const int64_t kb = cdiv(K, BLOCK), nb = cdiv(N, BLOCK);
   if (!ld_ok(lda, K) || !ld_ok(ldb, layoutB == MCG_K_CONTIG ? K : N) || !ld_ok(ldd, N) || !ld_ok(ldsa, kb) ||
@@ -242,7 +253,7 @@ int mcg_grouped_path(int dtype, int layoutA, int layoutB, int64_t G, int64_t M, 
                      int64_t lda, const void* B, int64_t ldb, int64_t strideB, int blockB, int dtypeD, int64_t* plan) {
   const bool f8 = f8_type(dtype);
   if ((!f8 && !f16_type(dtype)) || !float_out(dtypeD) || !valid_layout(layoutA) || !valid_layout(layoutB) ||
-      !sizes_ok(M, N, K) || M == 0 || N == 0 || G < 0 || G > MAX_GROUPS)
+      !sizes_ok(M, N, K) || M == 0 || N == 0 || G < 0 || G > MAX_GROUPS || !tiles_ok(f8 ? 1 : 2, M, G, N, G > 0))
     return -1;
   mcg::GroupArgs a = group_args(M, N, K, A, lda, B, ldb, nullptr, nullptr, N, dtypeD, 0.0);
   static const int32_t some = 0;
@@ -258,7 +269,7 @@ int mcg_grouped_path(int dtype, int layoutA, int layoutB, int64_t G, int64_t M, 
 int mcg_grouped_grad_path(int dtype, int64_t G, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
                           const void* B, int64_t ldb, int dtypeD, int64_t* plan) {
   if (!f16_type(dtype) || (dtypeD != dtype && dtypeD != MCG_F32) || !sizes_ok(M, N, K) || M == 0 || N == 0 || G <= 0 ||
-      G > MAX_GROUPS)
+      G > MAX_GROUPS || !grad_tiles_ok(G, M, N))
     return -1;
   mcg::GroupArgs a = group_args(M, N, K, A, lda, B, ldb, nullptr, nullptr, N, dtypeD, 0.0);
   a.groups = (int)G;

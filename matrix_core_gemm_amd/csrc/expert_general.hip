@@ -244,7 +244,6 @@ __global__ __launch_bounds__(256) void group_tiny_kernel(GroupArgs p, int la, in
 }
 
 namespace {
-constexpr int64_t MAX_BLOCKS = MANY_TILES;  // (a launch holds less than 2^32 threads)
 int64_t cdiv(int64_t x, int64_t y) { return (x + y - 1) / y; }
 }  // namespace
 
@@ -298,8 +297,8 @@ hipError_t launch_group_general(int dt, int la, int lb, bool grad, const GroupAr
 
 hipError_t launch_group_tiny(int dt, int la, int lb, bool grad, const GroupArgs& a, hipStream_t s) {
   const int64_t cols = cdiv(a.N, 256), z = grad ? a.groups : 1;
-  if (cols * z > MAX_BLOCKS) return hipErrorInvalidValue;
-  const int64_t most = MAX_BLOCKS / (cols * z), rows = a.M < most ? a.M : most;
+  if (cols * z > MANY_TILES) return hipErrorInvalidValue;
+  const int64_t most = MANY_TILES / (cols * z), rows = a.M < most ? a.M : most;
   const dim3 grid((unsigned)cols, (unsigned)(rows < 4096 ? rows : 4096), (unsigned)z);
   if (dt == DT_BF16) hipLaunchKernelGGL((group_tiny_kernel<DT_BF16, DT_BF16>), grid, dim3(256), 0, s, a, la, lb, (int)grad);
   else if (dt == DT_F16) hipLaunchKernelGGL((group_tiny_kernel<DT_F16, DT_F16>), grid, dim3(256), 0, s, a, la, lb, (int)grad);

@@ -35,7 +35,6 @@ bool f8_pipe_ok(const GroupArgs& a, int la, int lb) {
          4 * (lb == MCG_K_CONTIG ? 256 : kb) * a.ldsb < LIM;
 }
 
-
 // A choice and its modelled time.
 struct Timed {
   GroupPlan plan;
@@ -53,12 +52,12 @@ constexpr TileTime TIMES_16[] = {{256, 1.45, 1.45, 12.0}, {128, 1.0, 0.62, 8.0},
 constexpr TileTime TIMES_F8[] = {{256, 1.85, 1.85, 12.0}, {128, 1.2, 0.7, 8.0}, {64, 0.85, 0.58, 5.0}};
 constexpr TileTime TIMES_WIDE[] = {{128, 2.0, 1.2, 8.0}, {64, 1.3, 0.8, 6.0}};
 
-// tiles(t): tiles of t rows; nk K tiles each.
-template <int N, class F>
-Timed best_tile(const TileTime (&times)[N], int64_t nk, int64_t cols, int num_cu, int least, int most, F tiles) {
+// tiles(t), at_most(t): tiles of t rows, likely and at most; nk K tiles each.
+template <int N, class F, class G>
+Timed best_tile(const TileTime (&times)[N], int64_t nk, int64_t cols, int num_cu, int least, int most, F tiles, G at_most) {
   Timed best{{KERNEL_GENERAL, 0}, 0.0};
   for (const TileTime& t : times) {
-    if (t.tile < least || t.tile > most) continue;
+    if (t.tile < least || t.tile > most || !tiles_fit(at_most(t.tile), cols, t.tile == 256 ? 256 : 128)) continue;
     const int64_t n = tiles(t.tile) * cdiv(cols, t.tile == 256 ? 256 : 128);
     const int64_t at_once = t.tile == 256 ? num_cu : 2 * (int64_t)num_cu;
     const double us = n <= num_cu ? t.alone_us * (0.75 + 0.25 * (double)n / num_cu) * nk + t.fixed_us
@@ -89,6 +88,7 @@ GroupPlan general_plan(int most, int64_t cols, int num_cu, F tiles) {
 Timed best_few_rows(const GroupArgs& a, int64_t eb, int num_cu) {
   Timed best{{KERNEL_GENERAL, 0}, 0.0};
   for (int tile = 16; tile <= (eb == 1 ? 64 : 32); tile *= 2) {
+    if (!tiles_fit(most_tiles(a.M, a.groups, tile, a.offsets != nullptr), a.N, 32)) continue;
     const double per_cu = (double)likely_tiles(a, tile) * (double)cdiv(a.N, 32) / num_cu;
     const double us = 6.0 + (per_cu < 1.0 ? 1.0 : per_cu) * (0.7 + (32 + tile) * (double)(a.K * eb) / 28e3);
     if (best.plan.tile == 0 || us < best.us) best = {{KERNEL_ROWS, tile}, us};
@@ -106,18 +106,19 @@ GroupPlan plan_grouped(int dt, int la, int lb, const GroupArgs& a, int num_cu) {
   const bool few = chunks && rows <= 64 && la == MCG_K_CONTIG && lb == MCG_K_CONTIG &&
                    (eb == 2 || (a.blockB == SCALE_BLOCK && 4 * 256 * a.ldsa < LIM));
   auto tiles = [&](int t) { return likely_tiles(a, t); };
-  Timed best{general_plan(eb == 2 ? 128 : 64, a.N, num_cu, tiles), 0.0};
+  auto at_most = [&](int t) { return most_tiles(a.M, a.groups, t, a.offsets != nullptr); };
+  Timed best{general_plan(general_rows((int)eb), a.N, num_cu, tiles), 0.0};
   if (pipe) {
-    best = eb == 2              ? best_tile(TIMES_16, nk, a.N, num_cu, 64, 256, tiles)
-           : a.out == OUT_BF16 ? best_tile(TIMES_F8, nk, a.N, num_cu, 64, la == MCG_K_CONTIG ? 256 : 128, tiles)
-                               : best_tile(TIMES_WIDE, nk, a.N, num_cu, 64, 128, tiles);
+    best = eb == 2              ? best_tile(TIMES_16, nk, a.N, num_cu, 64, 256, tiles, at_most)
+           : a.out == OUT_BF16 ? best_tile(TIMES_F8, nk, a.N, num_cu, 64, la == MCG_K_CONTIG ? 256 : 128, tiles, at_most)
+                               : best_tile(TIMES_WIDE, nk, a.N, num_cu, 64, 128, tiles, at_most);
     // (the weights of four groups in five come from HBM, at 4.3 TB/s in these kernels' tiles of few rows)
     const double weights_us = 5.0 + 0.8 * (double)std::min<int64_t>(a.groups, a.M) * (double)(a.N * a.K * eb) / 4.3e6;
     best.us = std::max(best.us, weights_us);
   }
   if (few) {
     const Timed t = best_few_rows(a, eb, num_cu);
-    if (best.plan.kernel == KERNEL_GENERAL || t.us < best.us) best = t;
+    if (t.plan.tile && (best.plan.kernel == KERNEL_GENERAL || t.us < best.us)) best = t;
   }
   return best.plan;
 }
@@ -128,8 +129,8 @@ GroupPlan plan_grouped_grad(int dt, const GroupArgs& a, int num_cu) {
   if (a.K == 0 || a.M * eb < 16 || a.N * eb < 16) return {KERNEL_TINY, 1};
   auto tiles = [&](int t) { return a.groups * cdiv(a.M, t); };
   if (chunks_ok(2, a, MCG_MN_CONTIG, MCG_MN_CONTIG, 3) && a.M >= 64 && a.N >= 64)
-    return best_tile(TIMES_16, cdiv(a.K * eb, 128 * a.groups), a.N, num_cu, 128, 256, tiles).plan;
-  return general_plan(128, a.N, num_cu, tiles);
+    return best_tile(TIMES_16, cdiv(a.K * eb, 128 * a.groups), a.N, num_cu, 128, 256, tiles, tiles).plan;
+  return general_plan(general_rows((int)eb), a.N, num_cu, tiles);
 }
 
 hipError_t launch_grouped(int dt, int la, int lb, const GroupArgs& a, int num_cu, hipStream_t s) {

@@ -39,6 +39,14 @@ inline int64_t most_tiles(int64_t M, int64_t G, int64_t tile, bool grouped) {
   return (M - some) / tile + some;
 }
 
+// Tiles that a launch and its counters hold, and whether `rows` tile rows of N columns stay below
+// (with what the pipelined kernels round their number up to).
+constexpr int MANY_TILES = 1 << 23;
+inline bool tiles_fit(int64_t rows, int64_t N, int64_t cols) { return rows * ((N + cols - 1) / cols) + 64 < MANY_TILES; }
+
+// Rows of the general kernels' largest tiles (128 columns): a call whose tiles of that size do not fit is refused.
+inline int general_rows(int elem_bytes) { return elem_bytes == 2 ? 128 : 64; }
+
 // General kernels: any size, pointer and leading dimension (expert_general.hip).  dt: element
 // type of A (bf16, f16, or an 8-bit float; B is then E4M3).
 hipError_t launch_group_general(int dt, int la, int lb, bool grad, const GroupArgs& a, int tile, hipStream_t s);

@@ -6,6 +6,7 @@
 
 #include <type_traits>
 
+#include "experts.hpp"
 #include "tile_order.hpp"
 
 namespace mcg {
@@ -21,9 +22,8 @@ __host__ __device__ inline GroupRows group_rows(const int32_t* offsets, int g, i
   return GroupRows{r0, b < r0 ? r0 : b > M ? M : b};
 }
 
-// Tiles of tm rows of a group, and the most tiles that are counted in all: launches are
-// smaller, so that only offsets that decrease, and so count rows often, reach it.
-constexpr int MANY_TILES = 1 << 23;
+// Tiles of tm rows of a group.  (Launches are smaller than MANY_TILES: only offsets that decrease, and so
+// count rows often, reach it.)
 __host__ __device__ inline int tiles_of(const GroupRows& r, int tm) {
   const int64_t n = (r.r1 - r.r0 + tm - 1) / tm;
   return n < MANY_TILES ? (int)n : MANY_TILES;

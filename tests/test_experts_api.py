@@ -158,7 +158,7 @@ def test_path_queries_refuse_what_the_calls_refuse():
     assert m.grouped_path("f32", 0, 0, 2, 4, 64, 64, FAKE, 64, FAKE, 64, 0, 128, "f32")[0] == -1
     assert m.grouped_path("bf16", 0, 0, 2, 0, 64, 64, FAKE, 64, FAKE, 64, 0, 128, "bf16")[0] == -1
     assert m.grouped_grad_path("bf16", 0, 4, 64, 64, FAKE, 64, FAKE, 64, "bf16")[0] == -1
-    assert m.grouped_path("bf16", 0, 0, 2, 4, 64, 3, FAKE, 64, FAKE, 64, 0, 128, "bf16")[0] == 16
+    assert m.grouped_path("bf16", 0, 0, 2, 1, 64, 3, FAKE, 64, FAKE, 64, 0, 128, "bf16")[0] == 16
     assert m.grouped_grad_path("bf16", 2, 4, 64, 64, FAKE, 64, FAKE, 64, "bf16")[0] == 16
     assert m.lib().mcg_grouped_path(0, 0, 0, 2, 4, 64, 64, FAKE, 64, FAKE, 64, 0, 128, 0, ctypes.c_void_p(0)) >= 0
 
@@ -187,3 +187,19 @@ def test_plain_products_agree_with_loops():
     x, y = ref.rand(3, 9, 2), ref.rand(4, 9, 6)
     g, _ = ref.grouped_grad(x, y, off, None, 0.0)
     assert torch.allclose(g[0], sum(x[r][:, None] * y[r] for r in (1, 2))) and not g[1].any()
+
+
+@pytest.mark.parametrize("validate,base,fits,not_fit", [
+    (m.validate_quantize_blocks, QUANT, dict(M=1, N=128 * (2**24 - 1)), dict(M=1, N=128 * (2**24 - 1) + 1)),
+    (m.validate_f8_blocks, F8, dict(M=64 * 4096, N=128 * 2047), dict(M=64 * 4096, N=128 * 2048)),
+    (m.validate_grouped, GROUPED, dict(G=65535, M=65535, N=128 * 127), dict(G=65535, M=65535, N=128 * 128 + 1)),
+    (m.validate_grouped_grad, GRAD, dict(G=65535, M=128, N=128 * 127), dict(G=65535, M=129, N=128 * 64 + 1)),
+    (m.validate_grouped_f8_blocks, GROUPED8, dict(G=65535, M=65535 * 64, N=128 * 64), dict(G=65535, M=65535 * 64, N=128 * 65)),
+], ids=["quantize_blocks", "f8_blocks", "grouped", "grouped_grad", "grouped_f8_blocks"])
+def test_more_tiles_than_a_launch_holds_are_refused(validate, base, fits, not_fit):
+    big = 1 << 40  # leading dimensions and strides of any size
+    for sizes, status in ((fits, 0), (not_fit, 2)):
+        lds = {k: big for k in base if k.startswith("ld")}
+        if "strideD" in base:
+            lds["strideD"] = 1 << 60
+        check(validate, base, {**lds, **sizes}, status)

@@ -65,6 +65,26 @@ def test_the_choice_follows_the_work():
             assert kernel in (cases.FEW, cases.PIPE_64, cases.PIPE_128, cases.PIPE_256) and rows in (16, 32, 64, 128, 256)
 
 
+def test_a_launch_holds_the_tiles_of_the_choice():
+    """At the most rows, groups and columns that a call may have, and just below: fewer than 2^23 workgroups."""
+    for dt, dtD, most in (("bf16", "bf16", 128), ("e4m3", "bf16", 64), ("e4m3", "f32", 64)):
+        for G, M in ((65535, 65535), (65535, 200000), (65535, 1 << 22), (1000, 1000), (0, 64), (0, 1 << 20), (8, 1 << 25)):
+            def tiles(t):
+                some = min(max(G, 1), M)
+                return -(-M // t) if G == 0 else (M - some) // t + some
+            cols = (2**23 - 65) // tiles(most)
+            for N in (128 * cols, 64 * cols, 32 * cols, 128 * cols // 5 * 4 + 1):
+                if not 0 < N < 1 << 24:
+                    continue
+                for K in (16, 128, 1024):
+                    kernel, rows = m.grouped_path(dt, "k_contig", "k_contig", G, M, N, K, FAKE, K, FAKE, K, N * K, 128, dtD)
+                    assert kernel >= 0, (dt, G, M, N, K)
+                    if kernel != cases.TINY:
+                        wide = {cases.FEW: 32, cases.PIPE_256: 256}.get(kernel, 128)
+                        assert tiles(rows) * -(-N // wide) < 2**23, (dt, G, M, N, K, kernel, rows)
+            assert m.grouped_path(dt, "k_contig", "k_contig", G, M, 128 * cols + 1, 128, FAKE, 128, FAKE, 128, 0, 128, dtD)[0] == -1
+
+
 @pytest.mark.skipif(shutil.which(HIPCC) is None, reason="no hipcc")
 @pytest.mark.parametrize("source", ["blocks_quant.hip", "expert_rows.hip", "f8_blocks.hip"])
 def test_kernels_that_spill_nothing(tmp_path, source):
