@@ -628,3 +628,57 @@ def test_an_expert_layers_step_on_another_stream_and_in_a_graph(K, N, sizes):
     g.replay()
     same(changed, "replay with other offsets")
     say(f"  {K} x {N} {sizes}: same bits on other streams and in replays")
+
+
+# --------------------------------------------------------------------- the example
+def test_the_example_runs_and_its_gradients_hold():
+    """Gradients against the formulas over the tensors that the layer quantised, and against
+    differences of the forward product."""
+    need_gpu()
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "expert_layer.py")
+    spec = importlib.util.spec_from_file_location("expert_layer", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    T, K, N, G = 200, 192, 256, 5
+    layer = example.ExpertLayer(T, K, N, G)
+    x, dy = ref.rand(1, T, K).bfloat16().cuda(), ref.rand(2, T, N).bfloat16().cuda()
+    expert = torch.from_numpy(np.random.default_rng(3).integers(0, G - 1, T)).cuda()  # (one expert has no token)
+    y, dx = layer.forward(x, expert), layer.backward(dy)
+    torch.cuda.synchronize()
+    order, off = layer.order.cpu(), layer.offsets.cpu()
+    val = lambda q, to, s, bm, bn: ref.values(q.cpu(), to, s.cpu(), bm, bn)
+    w = torch.stack([val(layer.qw[g], "e4m3", layer.sw[g], BLOCK, BLOCK) for g in range(G)])
+    ws = val(layer.qws, "e4m3", layer.sws, BLOCK, BLOCK)
+    xq, dyq = val(layer.qx, "e4m3", layer.sx, 1, BLOCK), val(layer.qdy, "e5m2", layer.sdy, 1, BLOCK)
+    xt, dyt = val(layer.qxt, "e4m3", layer.sxt, BLOCK, 1), val(layer.qdyt, "e5m2", layer.sdyt, BLOCK, 1)
+
+    def two(a, b, bs, k):  # the experts' product, rounded, is the C of the shared one
+        d, mag = ref.grouped(a, b, off)
+        tol = ref.tol_f8(d, mag, k, "bf16")
+        return d + a @ bs, tol + ref.tol_f8(d + a @ bs, mag + a.abs() @ bs.abs(), k, "bf16") + 2 * ref.U["bf16"] * tol
+    exact, tol = two(xq, w.transpose(1, 2), ws.T, K)
+    within(y.cpu()[order], exact, tol, "y")
+    dx_exact, dx_tol = two(dyq, w, ws, N)
+    within(dx.cpu()[order], dx_exact, dx_tol, "dx")
+    dw, mag = ref.grouped_grad(layer.dy.cpu(), layer.x.cpu(), off, None, 0.0)
+    dw_tol = ref.tol_16(dw, mag, T, "f32")
+    within(layer.dw, dw, dw_tol, "dw")
+    dws, mags = dyt.T @ xt, dyt.abs().T @ xt.abs()
+    dws_tol = ref.tol_f8(dws, mags, T, "f32")
+    within(layer.dws, dws, dws_tol, "dws")
+    # sum of dy * y is linear in each of x, w and ws: a step along a direction changes it by the gradient's
+    # product with the direction
+    r = np.random.default_rng(4)
+    f = lambda X, W, WS, DY: float((DY * (ref.grouped(X, W.transpose(1, 2), off)[0] + X @ WS.T)).sum())
+    V = torch.from_numpy(r.standard_normal((T, K)))
+    change = (f(xq + V, w, ws, dyq) - f(xq - V, w, ws, dyq)) / 2
+    assert abs(float((dx.cpu()[order].double() * V).sum()) - change) <= float((dx_tol * V.abs()).sum()) * (1 + 1e-9)
+    V, xb, dyb = torch.from_numpy(r.standard_normal((G, N, K))), layer.x.cpu().double(), layer.dy.cpu().double()
+    change = (f(xb, w + V, ws, dyb) - f(xb, w - V, ws, dyb)) / 2
+    assert abs(float((layer.dw.cpu().double() * V).sum()) - change) <= float((dw_tol * V.abs()).sum()) * (1 + 1e-9)
+    V = torch.from_numpy(r.standard_normal((N, K)))
+    change = (f(xt, w, ws + V, dyt) - f(xt, w, ws - V, dyt)) / 2
+    assert abs(float((layer.dws.cpu().double() * V).sum()) - change) <= float((dws_tol * V.abs()).sum()) * (1 + 1e-9)
+    assert len(example.train(T=100, K=128, N=128, G=3, steps=2)) == 2
