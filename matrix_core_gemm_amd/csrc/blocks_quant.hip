@@ -15,7 +15,9 @@
 // 2^-52, and a quotient of two 24-bit values is never that near to the middle of two
 // binary32 values.
 //
-// Bound: memory (3 bytes per 16-bit element, 5 per binary32 one, each way).
+// Bound: memory (3 bytes per 16-bit element, 5 per binary32 one, each way): 8192 x 8192 bf16, 1 x 128 blocks,
+// and back 82 us, 4.96 TB/s (a copy 5.1).  A small matrix waits for its workgroups' one chain of loads, maximum
+// and stores: f16 333 x 2047, 128 x 1 blocks, and back 11.6 us, of which two launches are 6.
 #include "experts.hpp"
 #include "row_vec.hpp"
 

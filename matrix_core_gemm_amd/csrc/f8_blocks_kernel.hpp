@@ -24,6 +24,11 @@
 // largest of 8 consecutive products: off by 2^-12 of D, typically, where bf16 rounds at
 // 2^-8.  For f16 and binary32 D the codes are widened exactly to bf16 (WIDE), four
 // instructions of 32 k for a block.
+//
+// Bound: the matrix and the vector pipe together.  8192^3 to bf16 takes 527 us (2090 TFLOP/s), 494 with scales
+// that stay in registers, 418 with none; a weight gradient 4096^2 x 8192 to binary32 277 us (993
+// TFLOP/s).  Smaller calls: 500 x 4096 x 4096 in one round of 64 x 128 tiles 20.9 us, of which a K tile takes
+// 0.5; 8192 rows over 32 groups, 4096 x 4096, 234 us (the bytes alone 125).
 #pragma once
 #include "f8_block_ops.hpp"
 #include "fast_tiles.hpp"

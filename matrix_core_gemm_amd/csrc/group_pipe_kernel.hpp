@@ -5,12 +5,17 @@
 //   grad   D_g[i][j] = sum_{r in g} A[r][i] B[r][j] + beta C_g[i][j]
 //
 // Tile TB x TB by 8 (TB 256) or 4 (TB 128) wavefronts, each (TB / 2) x 64 outputs as 32 x 32 x
-// 16 instructions.  K tiles of 128 bytes of each row in two LDS stages, filled by
+// 16 instructions.  K tiles of 128 bytes of each row in two LDS stages (three of B), filled by
 // buffer_load ... lds.  A wavefront walks down its rows 32 by 32: the next rows' fragments
 // are read from LDS while 8 instructions (64 columns, whose fragments stay in registers) run
 // on these.  The K tile's barrier stands two rows of instructions before its end, where
 // the last fragments are in registers: its stage is then free for the K tile after next, and
 // the instructions that are left cover the barrier and the DMA's issue.
+//
+// Bound: the matrix pipe within a long tile (one group of 8192 rows, 8192 x 8192, 833 us, 1320 TFLOP/s; its
+// weight gradient 838); beside it a tile's prologue and epilogue, short last tiles and the last round
+// (8192 rows over 16 ragged groups, 4096 x 4096, 315 us, 253 with 512 rows each; their weight gradients, 8 K tiles
+// to a tile, 374).
 #pragma once
 #include "fast_tiles.hpp"
 #include "group_epilogue.hpp"
