@@ -17,7 +17,7 @@
 //
 // Bound: memory (3 bytes per 16-bit element, 5 per binary32 one, each way): 8192 x 8192 bf16, 1 x 128 blocks,
 // and back 82 us, 4.96 TB/s (a copy 5.1).  A small matrix waits for its workgroups' one chain of loads, maximum
-// and stores: f16 333 x 2047, 128 x 1 blocks, and back 11.6 us, of which two launches are 6.
+// and stores: f16 333 x 2047, 128 x 1 blocks, and back 8.9 us, of which two launches are 6.
 #include "experts.hpp"
 #include "row_vec.hpp"
 
@@ -142,7 +142,8 @@ __global__ __launch_bounds__(THREADS) void blocks_quant_kernel(BlocksArgs p) {
       raw[r] = get<DT, SHORT>(p.X + m * p.ldx * ES, c, p.N, at);
     }
     uint32_t top[8] = {};  // COL_BLOCKS: of each column
-    BlockStat s[KIND == ROW_BLOCKS ? RPT : 1];
+    uint32_t mine = 0;       // ROW_BLOCKS: of row tx of this thread's RPT
+    BlockStat s[1];
 #pragma unroll
     for (int r = 0; r < RPT; ++r) {
       float x[8];
@@ -160,16 +161,21 @@ __global__ __launch_bounds__(THREADS) void blocks_quant_kernel(BlocksArgs p) {
         uint32_t t = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) t = umax(t, top[e]);
-        s[r] = block_stat<DTQ>(row_umax(t));
+        t = row_umax(t);
+        mine = tx == r ? t : mine;
       }
     }
-    float lead[8];
-    double inv[8];
+    float lead[8], row_lead[RPT];
+    double inv[8], row_inv[RPT];
     if constexpr (KIND == ROW_BLOCKS) {
+      // (each of a row's lanes finds another row's scale, and hands it to all 16)
+      s[0] = block_stat<DTQ>(mine);
+      const int64_t m = m0 + ty + TY * tx;
+      if (tx < RPT && m < p.M) p.scale[m * p.lds + blockIdx.x] = s[0].scale;
 #pragma unroll
       for (int r = 0; r < RPT; ++r) {
-        const int64_t m = m0 + ty + TY * r;
-        if (tx == 0 && m < p.M) p.scale[m * p.lds + blockIdx.x] = s[r].scale;
+        row_lead[r] = __shfl(s[0].lead, r, 16);
+        row_inv[r] = __shfl(s[0].inv, r, 16);
       }
     } else {
       __shared__ uint32_t lt[TY][COLS];
@@ -192,20 +198,31 @@ __global__ __launch_bounds__(THREADS) void blocks_quant_kernel(BlocksArgs p) {
         }
         if (threadIdx.x == 0) p.scale[m0 / SCALE_BLOCK * p.lds + blockIdx.x] = s[0].scale;
       } else {
-        // columns, 8 by 8 as the lanes hold them (a shifted vector's are its own)
+        // columns, 8 by 8 as the lanes hold them (a shifted vector's are its own); a thread finds the scale of
+        // one (all 8 in each thread, with as many binary64 quotients: 333 x 2047 7.1 us, so 5.1)
+        __shared__ __attribute__((aligned(16))) double linv[COLS];
+        __shared__ __attribute__((aligned(16))) float llead[COLS];
 #pragma unroll
         for (int e = 0; e < 8; ++e) lt[ty][8 * tx + e] = top[e];
         __syncthreads();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        if (threadIdx.x < COLS) {
+          const int slot = threadIdx.x, e = slot & 7;
           uint32_t t = 0;
 #pragma unroll
-          for (int r = 0; r < TY; ++r) t = umax(t, lt[r][8 * tx + e]);
+          for (int r = 0; r < TY; ++r) t = umax(t, lt[r][slot]);
           s[0] = block_stat<DTQ>(t);
-          lead[e] = s[0].lead;
-          inv[e] = s[0].inv;
-          const int64_t n = SHORT ? c + e : at.at + e;
-          if (ty == 0 && e >= at.skip && n < p.N) p.scale[m0 / SCALE_BLOCK * p.lds + n] = s[0].scale;
+          linv[slot] = s[0].inv;
+          llead[slot] = s[0].lead;
+          const int64_t c8 = (int64_t)blockIdx.x * COLS + (slot - e);
+          const RowVec mine = SHORT ? RowVec{c8, c8 < p.N ? 0 : 8} : row_vec(c8, p.N);
+          const int64_t n = mine.at + e;
+          if (e >= mine.skip && n < p.N) p.scale[m0 / SCALE_BLOCK * p.lds + n] = s[0].scale;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          lead[e] = llead[8 * tx + e];
+          inv[e] = linv[8 * tx + e];
         }
       }
     }
@@ -218,8 +235,8 @@ __global__ __launch_bounds__(THREADS) void blocks_quant_kernel(BlocksArgs p) {
       if constexpr (KIND == ROW_BLOCKS) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          lead[e] = s[r].lead;
-          inv[e] = s[r].inv;
+          lead[e] = row_lead[r];
+          inv[e] = row_inv[r];
         }
       }
       const i32x2 q = codes8<DTQ>(x, lead, inv);
@@ -238,17 +255,27 @@ __global__ __launch_bounds__(THREADS) void blocks_dequant_kernel(BlocksArgs p) {
   const int64_t first = SHORT ? c : at.at;
   for (int64_t m0 = (int64_t)blockIdx.y * (RPT * TY); m0 < p.M; m0 += (int64_t)gridDim.y * (RPT * TY)) {
     Raw8<DT_I8> raw[RPT];
-    float s[RPT][KIND == COL_BLOCKS ? 8 : 1];
+    float s[KIND == COL_BLOCKS ? 8 : RPT];
+    if constexpr (KIND == COL_BLOCKS) {
+      // (the rows of a step lie in one block; a whole vector in two loads: each scale by its own, for every
+      // row, 8192 x 4096 63 us, so 16)
+      static_assert(SCALE_BLOCK % (RPT * TY) == 0, "rows of one block");
+      const float* sc = p.scale + m0 / SCALE_BLOCK * p.lds;
+      if constexpr (SHORT) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = sc[min(first + e, p.N - 1)];
+      } else {
+        typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+        const f32x4_any lo = *(const f32x4_any*)(sc + first), hi = *(const f32x4_any*)(sc + first + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = lo[e], s[4 + e] = hi[e];
+      }
+    }
 #pragma unroll
     for (int r = 0; r < RPT; ++r) {
       const int64_t m = min(m0 + ty + TY * r, p.M - 1);
       raw[r] = get<DT_I8, SHORT>(p.X + m * p.ldx, c, p.N, at);
-      if constexpr (KIND == COL_BLOCKS) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s[r][e] = p.scale[m / SCALE_BLOCK * p.lds + min(first + e, p.N - 1)];
-      } else {
-        s[r][0] = p.scale[(KIND == ROW_BLOCKS ? m : m / SCALE_BLOCK) * p.lds + blockIdx.x];
-      }
+      if constexpr (KIND != COL_BLOCKS) s[r] = p.scale[(KIND == ROW_BLOCKS ? m : m / SCALE_BLOCK) * p.lds + blockIdx.x];
     }
 #pragma unroll
     for (int r = 0; r < RPT; ++r) {
@@ -258,7 +285,7 @@ __global__ __launch_bounds__(THREADS) void blocks_dequant_kernel(BlocksArgs p) {
       values8<DTQ>(raw[r], x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        x[e] *= s[r][KIND == COL_BLOCKS ? e : 0];
+        x[e] *= s[KIND == COL_BLOCKS ? e : r];
         // (else the compiler joins the product and the conversion in an instruction that rounds once,
         // for f16 alone)
         if constexpr (DT == DT_F16) asm volatile("" : "+v"(x[e]));
@@ -284,8 +311,12 @@ static hipError_t launch(const BlocksArgs& a, hipStream_t s) {
 template <bool QUANT, int DT, int DTQ>
 static hipError_t launch_kind(int bm, int bn, const BlocksArgs& a, hipStream_t s) {
   constexpr int RPT = SCALE_BLOCK / TY;
+  // Codes of rows: 4 rows a thread where that leaves four workgroups for each compute unit (2048 x 4096 bf16 6.8 us, 7.8 with
+  // 2 and 7.3 with 8; 333 x 2047 3.7, 3.2 with 2).
+  if (QUANT && bm == 1 && (a.M + 4 * TY - 1) / (4 * TY) * ((a.N + COLS - 1) / COLS) >= 1024)
+    return launch<QUANT, DT, DTQ, ROW_BLOCKS, QUANT ? 4 : 2>(a, s);
   if (bm == 1) return launch<QUANT, DT, DTQ, ROW_BLOCKS, 2>(a, s);
-  return bn == 1 ? launch<QUANT, DT, DTQ, COL_BLOCKS, QUANT ? RPT : 2>(a, s)
+  return bn == 1 ? launch<QUANT, DT, DTQ, COL_BLOCKS, QUANT ? RPT : 4>(a, s)
                  : launch<QUANT, DT, DTQ, SQUARE_BLOCKS, QUANT ? RPT : 2>(a, s);
 }
 template <bool QUANT>

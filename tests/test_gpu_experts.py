@@ -93,6 +93,24 @@ def test_blocks(dt, to, kind):
                 assert torch.equal(D.cpu(), v), f"values {M} x {N} {dtD}"
 
 
+@pytest.mark.parametrize("dt,to", [("bf16", "e4m3"), ("f16", "e5m2"), ("f32", "e4m3")])
+def test_blocks_of_many_rows(dt, to):
+    """1 x 128 blocks with more rows in a thread (over 1024 workgroups of 64 rows x 128 columns)."""
+    mcg = need_gpu()
+    M, N = 7003, 1187
+    x = (ref.rand(5, M, N) * torch.exp(ref.rand(6, N))).to(DT[dt])
+    x[M - 1, N - 1], x[70, 130] = float("inf"), float("nan")
+    X, Q, S = put(x, 5, 1), buf(M, N, torch.uint8, 5, 1), buf(M, cdiv(N, BLOCK), torch.float32, 1)
+    mcg.quantize_blocks(dt, to, 1, BLOCK, M, N, X, ld(X), Q, ld(Q), S, ld(S))
+    guards_hold(Q, S)
+    for r, c in ((M - 1, 9), (70, 1)):  # no numbers: scale NaN, codes 0
+        assert bool(torch.isnan(S[r, c])) and not bool(Q[r, BLOCK * c:BLOCK * (c + 1)].any())
+        x[r, BLOCK * c:BLOCK * (c + 1)] = 0
+        S[r, c] = 0
+    q, scale = ref.quantize(x, to, 1, BLOCK)
+    assert torch.equal(S.cpu(), scale) and torch.equal(Q.cpu(), q)
+
+
 @pytest.mark.parametrize("kind", list(KINDS))
 @pytest.mark.parametrize("to", ["e4m3", "e5m2"])
 def test_blocks_of_nothing_and_of_no_number(to, kind):
