@@ -48,8 +48,6 @@ mcg::GroupArgs group_args(int64_t M, int64_t N, int64_t K, const void* A, int64_
   a.alpha_i = 1;
   a.use_c = beta != 0.0;
   a.out = out_format(dtypeD);
-  const int vb = 4 * elem_bytes(dtypeD);
-  a.vec_cd = aligned_to(D, vb) && (!a.use_c || aligned_to(C, vb)) && ldd % 4 == 0;
   a.splits = 1;
   a.groups = 1;
   a.blockB = (int)BLOCK;
@@ -164,7 +162,6 @@ int gemm_grouped_grad(int dtype, int64_t G, int64_t M, int64_t N, int64_t K, con
   a.offsets = K > 0 ? offsets : nullptr;
   a.groups = (int)G;
   a.strideD = strideD;
-  a.vec_cd = a.vec_cd && (G == 1 || strideD % 4 == 0);
   return hip_status(mcg::launch_grouped_grad(dtype, a, current_num_cu(), (hipStream_t)stream));
 }
 
